@@ -258,6 +258,121 @@ ra_status ra_swc_cache_copy_rings_to_host(const ra_swc_cache* c, void* K_host, v
 ra_status ra_swc_cache_reset(ra_swc_cache* c);
 void ra_swc_cache_free(ra_swc_cache* c);
 
+/*
+ * Norm and rotation of Q and K, from the projection's rows to the attention's.
+ *
+ * ra_rope -- rotary positions over the three axes of a frame-major token
+ *   sequence.  Token i of a call lies in frame frame0 + i / (grid_h * grid_w), at
+ *   row and column of the row-major frame.  The channel pairs (2 i, 2 i + 1) of a
+ *   head are shared out among the axes: the first t_pairs follow the frame, the
+ *   next h_pairs the row, the next w_pairs the column, and the rest are not
+ *   rotated (t_pairs + h_pairs + w_pairs in [1, d / 2]).  t, h, w are device
+ *   tables of (cos, sin) fp32 pairs, [frames | grid_h | grid_w][pairs][2]; a table
+ *   of an axis without pairs is not read and may be NULL.
+ * ra_rope_table -- fill such a table: (cos, sin) of p * base^(-i / pairs) for the
+ *   positions p = start .. start + length - 1 and i = 0 .. pairs - 1, with the
+ *   angle in 64 bits (pairs in [1, 64], base > 1).
+ * ra_head_rows -- a strided bf16 tensor [B, n, heads, d]: strides in elements,
+ *   multiples of 8, >= 0 (0 broadcasts); channels contiguous; 16-byte aligned.
+ *   weight: the norm's [d] weight, bf16 or (weight_fp32 != 0) fp32, 16-byte
+ *   aligned, shared by the heads; NULL: no norm.
+ * ra_qk_norm_rope -- for every row x of q, and of k unless NULL (its number of
+ *   heads may differ):
+ *     y = R(position) (x * weight / sqrt(mean(x^2) + eps)),
+ *   computed in fp32 and rounded once, written to q_out, k_out: bf16
+ *   [B, heads, n, d], contiguous, 16-byte aligned, aliasing nothing else of the
+ *   call.  A tensor without a weight is only rotated; rope NULL: no rotation (one
+ *   of the two is needed).  eps > 0.  n = 0 is allowed.
+ * ra_qk_norm_rope_bwd -- the gradient of that call, given the gradients dy of its
+ *   outputs (bf16 [B, heads, n, d], contiguous): dx by its own strides (bf16
+ *   [B, n, heads, d]; no two rows may overlap; dq and dk may be slots of one packed
+ *   buffer) and, with a weight, dweight (fp32 [d], written, the sum over batch,
+ *   tokens and heads).  x, weight, rope, frame0 and eps as in the forward call
+ *   (nothing else is kept from it).  workspace: caller-owned device memory of
+ *   ra_qk_norm_rope_bwd_workspace_bytes(d), 16-byte aligned, needed when there is a
+ *   weight; calls that may overlap on the GPU need one each.
+ * d is 64 or 128.  Deterministic (no atomics); asynchronous on `stream`; no
+ * allocation, so the calls may be captured into a CUDA graph.
+ */
+typedef struct {
+    const float* t;
+    const float* h;
+    const float* w;
+    int frames, grid_h, grid_w;
+    int t_pairs, h_pairs, w_pairs;
+} ra_rope;
+
+typedef struct {
+    const void* x;
+    long long stride_b, stride_n, stride_h;
+    int heads;
+    int weight_fp32;
+    const void* weight;
+} ra_head_rows;
+
+typedef struct {
+    const void* dy;
+    void* dx;
+    long long stride_b, stride_n, stride_h; /* of dx */
+    float* dweight;
+} ra_head_grads;
+
+ra_status ra_rope_table(float* table, int start, int length, int pairs, double base, ra_stream stream);
+ra_status ra_qk_norm_rope(const ra_head_rows* q, const ra_head_rows* k, void* q_out, void* k_out, int B, int n, int d,
+                          const ra_rope* rope, int frame0, float eps, ra_stream stream);
+size_t ra_qk_norm_rope_bwd_workspace_bytes(int d);
+ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, const ra_head_grads* dq,
+                              const ra_head_grads* dk, int B, int n, int d, const ra_rope* rope, int frame0, float eps,
+                              void* workspace, size_t workspace_bytes, ra_stream stream);
+
+/*
+ * The 8-bit key/value ring: the streaming window in half the memory.
+ *
+ * A ring holds W = window_frames frames of s tokens for B x H heads of d (64 or
+ * 128) channels, in four caller-owned device buffers:
+ *   k8, v8           : e4m3 codes [B, H, W * s, d], 16-byte aligned; frame i in
+ *                      slot i mod W, rows (i mod W) * s ..
+ *   k_scale, v_scale : fp32 [B, H, W, ceil(s / 64)]: one scale for each block of 64
+ *                      tokens of a slot (the last one of a slot may be shorter) and
+ *                      head.  A code stands for code * scale.
+ * Scales are powers of two, so that code * scale is a bf16 number; another
+ * positive scale is rounded to bf16, as is the product.  The two e4m3 codes of NaN
+ * are not used (they read as +-480); a scale of NaN makes its block NaN.
+ *
+ * ra_cache8_append -- `frames` new frames (1 .. W), the first being frame number
+ *   `frame` >= 0 of the stream, into their slots.  k, v: strided bf16
+ *   [B, frames * s, H, d] (see ra_head_rows; v's weight must be NULL).  K is normed
+ *   (k->weight) and rotated (rope: grid_h * grid_w = s, time position = frame
+ *   number) as by ra_qk_norm_rope, either may be left out, and both K and V are
+ *   rounded once, from fp32 to the nearest code (ties to even).  The scale of a
+ *   block is the least power of two, not below 2^-126, that brings its largest
+ *   magnitude to at most 448; 1 for a block of zeros; NaN (with codes 0) for one
+ *   with an infinity or a NaN.  Slots of other frames are left as they are.
+ * ra_cache8_attention -- O = softmax(scale * Q K^T) V of nq (1 .. 2^24) queries per
+ *   head over the frames in slots 0 .. held - 1 (held in [0, W]; after i + 1 frames
+ *   held = min(i + 1, W): the window of RA_MASK_SWC).
+ *   Q, O       : device bf16 [B, H, nq, d], contiguous, 16-byte aligned; O written.
+ *   key_counts : NULL, or device int32 [B]: batch element b attends to the first
+ *                key_counts[b] rows only (clamped to [0, held * s]).
+ *   lse        : NULL, or device fp32 [B, H, nq] (natural log).
+ *   A query without keys gets O = 0 and lse = -inf.
+ *   workspace  : caller-owned device memory of ra_cache8_attention_workspace_bytes
+ *                for the same sizes (0 for some), 16-byte aligned; calls that may
+ *                overlap on the GPU need one each.
+ * No output may alias another buffer of the call.  Deterministic (no atomics);
+ * asynchronous on `stream`; no allocation, so the calls may be captured into a CUDA
+ * graph (which replays them with the same frame and held).
+ */
+ra_status ra_cache8_append(const ra_head_rows* k, const ra_head_rows* v, int B, int frames, int d, int s,
+                           int window_frames, long long frame, const ra_rope* rope, float eps, void* k8, void* v8,
+                           float* k_scale, float* v_scale, ra_stream stream);
+ra_status ra_cache8_attention_workspace_bytes(int B, int H, int d, int nq, int s, int window_frames, int held,
+                                              size_t* bytes);
+ra_status ra_cache8_attention(const void* Q, const void* k8, const void* v8, const float* k_scale,
+                              const float* v_scale, void* O, int B, int H, int d, int nq, int s, int window_frames,
+                              int held, const int* key_counts, float scale, float* lse, void* workspace,
+                              size_t workspace_bytes, ra_stream stream);
+
 /* Synchronise `stream`, then read and clear the current device's error word.
  * RA_ERR_DEVICE_TIMEOUT if a kernel gave up a bounded wait since the last call. */
 ra_status ra_get_device_status(ra_stream stream);

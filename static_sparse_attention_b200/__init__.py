@@ -12,9 +12,11 @@ compiled library is missing (build it with
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 # RA_LIBRARY_VARIANT=debug selects the build with device-side bounds checks
@@ -54,6 +56,23 @@ class ra_mask_info_t(ctypes.Structure):
                 ("row_min", ctypes.c_int), ("row_max", ctypes.c_int)]
 
 
+class ra_rope(ctypes.Structure):
+    _fields_ = [("t", ctypes.c_void_p), ("h", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("frames", ctypes.c_int), ("grid_h", ctypes.c_int), ("grid_w", ctypes.c_int),
+                ("t_pairs", ctypes.c_int), ("h_pairs", ctypes.c_int), ("w_pairs", ctypes.c_int)]
+
+
+class ra_head_rows(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_n", ctypes.c_longlong),
+                ("stride_h", ctypes.c_longlong), ("heads", ctypes.c_int), ("weight_fp32", ctypes.c_int),
+                ("weight", ctypes.c_void_p)]
+
+
+class ra_head_grads(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_n", ctypes.c_longlong), ("stride_h", ctypes.c_longlong), ("dweight", ctypes.c_void_p)]
+
+
 _vp, _i, _ll, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_float
 _MaskP = ctypes.c_void_p
 _SIGS = {
@@ -75,6 +94,14 @@ _SIGS = {
     "ra_swc_cache_copy_rings_to_host": ([_vp, _vp, _vp], _i),
     "ra_swc_cache_reset": ([_vp], _i),
     "ra_swc_cache_free": ([_vp], None),
+    "ra_rope_table": ([_vp, _i, _i, _i, ctypes.c_double, _vp], _i),
+    "ra_qk_norm_rope": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp], _i),
+    "ra_qk_norm_rope_bwd_workspace_bytes": ([_i], ctypes.c_size_t),
+    "ra_qk_norm_rope_bwd": ([_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _i, _f, _vp, ctypes.c_size_t, _vp], _i),
+    "ra_cache8_append": ([_vp, _vp, _i, _i, _i, _i, _i, _ll, _vp, _f, _vp, _vp, _vp, _vp, _vp], _i),
+    "ra_cache8_attention_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)], _i),
+    "ra_cache8_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
+                             ctypes.c_size_t, _vp], _i),
     "ra_get_device_status": ([_vp], _i),
     "ra_get_device_error_site": ([ctypes.POINTER(_i), ctypes.POINTER(_i)], _i),
     "ra_selftest_wait_timeout": ([_ll, _vp], _i),
@@ -106,9 +133,47 @@ def check(status: int, where: str) -> None:
 
 def _stream_handle(stream) -> int | None:
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without making a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _allocating_on(stream, handle: int):
+    """Torch work inside is on `stream` (the current one when None): memory that a
+    call allocates and drops again is reused only behind the call's own work."""
+    if stream is None:
+        return _NO_CONTEXT
+    import torch
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return _NO_CONTEXT
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream())
+
+
+def _refuse_capture(stream) -> None:
+    import torch
+    with _allocating_on(stream, 0 if stream is None else _stream_handle(stream)):
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the cache's frame number is host state: a captured step would repeat it")
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _workspace(given, need: int, device, stream, handle: int):
+    """The caller's workspace, checked, or one of `need` bytes (None when none is needed)."""
+    import torch
+    if given is not None:
+        if not given.is_contiguous() or given.device != device or given.numel() * given.element_size() < need:
+            raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on {device}")
+        return given
+    if need == 0:
+        return None
+    with _allocating_on(stream, handle):
+        return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 # ------------------------------------------------------------------- masks
@@ -310,6 +375,339 @@ class SwcCache:
             self.free()
         except Exception:
             pass
+
+
+# ------------------------------------------- norm and rotation of Q and K
+class Rope3D(NamedTuple):
+    """Position tables of the time, height and width axes: contiguous fp32 CUDA
+    tensors [frames | grid_h | grid_w, pairs, 2] of (cos, sin).  Any tuple of
+    three such tensors does in its place."""
+    t: object
+    h: object
+    w: object
+
+
+def rope_axes(d: int) -> tuple:
+    """Channels of the time, height and width axes of a head of d channels when
+    none are named: height and width 2 * (d // 6) each, time the rest."""
+    return d - 4 * (d // 6), 2 * (d // 6), 2 * (d // 6)
+
+
+def rope3d(frames: int, grid_h: int, grid_w: int, d: int, axes=None, base: float = 10000.0, stream=None) -> Rope3D:
+    """Tables for `frames` frames of grid_h x grid_w tokens: pair i of an axis of
+    c channels turns by position * base^(-2 i / c).  axes: channels of each axis
+    (even, at most d together)."""
+    import torch
+    axes = rope_axes(d) if axes is None else tuple(axes)
+    if len(axes) != 3 or any(c < 0 or c % 2 for c in axes) or not 0 < sum(axes) <= d:
+        raise ValueError("axes must be three even numbers of channels, at most d together")
+    handle = _stream_handle(stream)
+    tables = []
+    for length, c in zip((frames, grid_h, grid_w), axes):
+        if length < 1:
+            raise ValueError("frames, grid_h and grid_w must be >= 1")
+        with _allocating_on(stream, handle):
+            table = torch.empty((length, c // 2, 2), dtype=torch.float32, device="cuda")
+        if c:
+            check(ra_rope_table(table.data_ptr(), 0, length, c // 2, float(base), handle), "ra_rope_table")
+        tables.append(table)
+    return Rope3D(*tables)
+
+
+def _rope_arg(rope, device):
+    """The C description of the tables (None without a rotation)."""
+    import torch
+    if rope is None:
+        return None
+    if len(rope) != 3:
+        raise ValueError("rope must be the tables of three axes")
+    for t in rope:
+        if t.dtype != torch.float32 or t.dim() != 3 or t.shape[2] != 2 or not t.is_contiguous() or t.device != device:
+            raise ValueError("rope tables must be contiguous fp32 tensors [positions, pairs, 2] on the inputs' device")
+    t, h, w = rope
+    return ra_rope(t.data_ptr(), h.data_ptr(), w.data_ptr(), t.shape[0], h.shape[0], w.shape[0], t.shape[1],
+                   h.shape[1], w.shape[1])
+
+
+def _rows_arg(name, x, weight, d, device):
+    """The C description of a strided [B, n, H, d] tensor and its norm weight."""
+    import torch
+    if x.dtype != torch.bfloat16 or not x.is_cuda or x.dim() != 4 or x.shape[3] != d or x.stride(3) != 1:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [B, n, H, d] with contiguous channels")
+    if x.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    w, fp32 = None, 0
+    if weight is not None:
+        if weight.dtype not in (torch.bfloat16, torch.float32) or tuple(weight.shape) != (d,) \
+                or not weight.is_contiguous() or weight.device != device:
+            raise ValueError(f"the weight of {name} must be a contiguous bf16 or fp32 tensor [d] on {device}")
+        w, fp32 = weight.data_ptr(), int(weight.dtype == torch.float32)
+    sb, sn, sh, _ = x.stride()
+    return ra_head_rows(x.data_ptr(), sb, sn, sh, x.shape[2], fp32, w)
+
+
+def _current_device(x):
+    """The inputs' device, which has to be the current one (the library launches there)."""
+    import torch
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    return x.device
+
+
+def _head_major_out(name, out, shape, device, stream, handle):
+    import torch
+    if out is None:
+        with _allocating_on(stream, handle):
+            return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    _check_bf16_cuda(name, out)
+    if tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"{name} must have shape {tuple(shape)} on {device}")
+    return out
+
+
+def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, frame0: int = 0, eps: float = 1e-6, q_out=None,
+                 k_out=None, stream=None):
+    """Per-head RMS norm and 3-axis rotation of the projections q and k (bf16
+    [B, n, H, d], any strides with contiguous channels, such as slices of a fused
+    projection): returns (q, k) as bf16 [B, H, n, d], ready for attention_fwd.
+
+    A weight (bf16 or fp32 [d]) turns the norm of its tensor on; rope (rope3d, or
+    three tables) the rotation, the first token being the first of frame `frame0`.
+    k may be left out (None is returned in its place)."""
+    device = _current_device(q)
+    if q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n, H, d]")
+    B, n, H, d = q.shape
+    if k is not None and (k.dim() != 4 or tuple(k.shape[:2]) != (B, n)):
+        raise ValueError("k must be a tensor [B, n, Hk, d] with q's B and n")
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out need k")
+    handle = _stream_handle(stream)
+    rows_q = _rows_arg("q", q, q_weight, d, device)
+    rows_k = None if k is None else _rows_arg("k", k, k_weight, d, device)
+    table = _rope_arg(rope, device)
+    q_out = _head_major_out("q_out", q_out, (B, H, n, d), device, stream, handle)
+    if k is not None:
+        k_out = _head_major_out("k_out", k_out, (B, k.shape[2], n, d), device, stream, handle)
+    if n == 0:
+        return q_out, k_out
+    check(ra_qk_norm_rope(_ref(rows_q), _ref(rows_k), q_out.data_ptr(), None if k is None else k_out.data_ptr(), B, n,
+                          d, _ref(table), frame0, eps, handle), "ra_qk_norm_rope")
+    return q_out, k_out
+
+
+def _grads_arg(name, rows, dy, dx, like, dweight, device, stream, handle):
+    """The C description of one tensor's gradients; allocates dx and dweight when they are not given."""
+    import torch
+    B, n, H, d = like.shape
+    _check_bf16_cuda("d" + name + "_out", dy)
+    if tuple(dy.shape) != (B, H, n, d) or dy.device != device:
+        raise ValueError(f"d{name}_out must have shape {(B, H, n, d)} on {device}")
+    if dx is None:
+        with _allocating_on(stream, handle):
+            dx = torch.empty((B, n, H, d), dtype=torch.bfloat16, device=device)
+    if dx.dtype != torch.bfloat16 or dx.device != device or tuple(dx.shape) != (B, n, H, d) or dx.stride(3) != 1:
+        raise ValueError(f"d{name} must be a bf16 tensor {(B, n, H, d)} on {device} with contiguous channels")
+    if rows.weight is None:
+        if dweight is not None:
+            raise ValueError(f"d{name}_weight needs a weight of {name}")
+    elif dweight is None:
+        with _allocating_on(stream, handle):
+            dweight = torch.empty(d, dtype=torch.float32, device=device)
+    elif dweight.dtype != torch.float32 or tuple(dweight.shape) != (d,) or not dweight.is_contiguous() \
+            or dweight.device != device:
+        raise ValueError(f"d{name}_weight must be a contiguous fp32 tensor [d] on {device}")
+    sb, sn, sh, _ = dx.stride()
+    return dx, dweight, ra_head_grads(dy.data_ptr(), dx.data_ptr(), sb, sn, sh,
+                                      None if dweight is None else dweight.data_ptr())
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=None, frame0: int = 0, eps: float = 1e-6,
+                     dq=None, dk=None, dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Gradient of qk_norm_rope: from dq_out, dk_out (bf16 [B, H, n, d], as
+    attention_bwd returns them) to (dq, dk, dq_weight, dk_weight): dq, dk bf16
+    [B, n, H, d] (given ones may be strided, such as slices of one packed gradient)
+    and fp32 [d] for each weight (None without one).  q, k, the weights, rope,
+    frame0 and eps as in the forward call; k and dk_out may both be None."""
+    import torch
+    device = _current_device(q)
+    if q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n, H, d]")
+    B, n, H, d = q.shape
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    if k is not None and (k.dim() != 4 or tuple(k.shape[:2]) != (B, n)):
+        raise ValueError("k must be a tensor [B, n, Hk, d] with q's B and n")
+    if k is None and any(x is not None for x in (k_weight, dk, dk_weight)):
+        raise ValueError("k_weight, dk and dk_weight need k")
+    handle = _stream_handle(stream)
+    rows_q = _rows_arg("q", q, q_weight, d, device)
+    rows_k = None if k is None else _rows_arg("k", k, k_weight, d, device)
+    table = _rope_arg(rope, device)
+    dq, dq_weight, grads_q = _grads_arg("q", rows_q, dq_out, dq, q, dq_weight, device, stream, handle)
+    grads_k = None
+    if k is not None:
+        dk, dk_weight, grads_k = _grads_arg("k", rows_k, dk_out, dk, k, dk_weight, device, stream, handle)
+    if n == 0:
+        for w in (dq_weight, dk_weight):
+            if w is not None:
+                with _allocating_on(stream, handle):
+                    w.zero_()
+        return dq, dk, dq_weight, dk_weight
+    need = ra_qk_norm_rope_bwd_workspace_bytes(d) if q_weight is not None or k_weight is not None else 0
+    workspace = _workspace(workspace, need, device, stream, handle)
+    check(ra_qk_norm_rope_bwd(_ref(rows_q), _ref(rows_k), _ref(grads_q), _ref(grads_k), B, n, d, _ref(table), frame0,
+                              eps, None if workspace is None else workspace.data_ptr(), need, handle),
+          "ra_qk_norm_rope_bwd")
+    return dq, dk, dq_weight, dk_weight
+
+
+# ------------------------------------------------------- 8-bit key/value ring
+CACHE8_BLOCK = 64  # tokens of a frame that share a scale
+
+
+def _ring_shape(k8, v8, k_scale, v_scale, device):
+    """(B, H, d, s, W) of an 8-bit ring, checked."""
+    import torch
+    if k8.dim() != 4 or k_scale.dim() != 4:
+        raise ValueError("k8 must be [B, H, W * s, d] and k_scale [B, H, W, ceil(s / 64)]")
+    B, H, rows, d = k8.shape
+    W, blocks = k_scale.shape[2:]
+    s = rows // W if W else 0
+    if s < 1 or rows != s * W or tuple(k_scale.shape) != (B, H, W, -(-s // CACHE8_BLOCK)):
+        raise ValueError("k_scale must be [B, H, W, ceil(s / 64)] for k8 [B, H, W * s, d]")
+    for name, t, like, dtype in (("k8", k8, k8, torch.float8_e4m3fn), ("v8", v8, k8, torch.float8_e4m3fn),
+                                 ("k_scale", k_scale, k_scale, torch.float32),
+                                 ("v_scale", v_scale, k_scale, torch.float32)):
+        if t.dtype is not dtype or t.shape != like.shape or not t.is_contiguous() or t.device != device:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(like.shape)} on {device}")
+    return B, H, d, s, W
+
+
+def cache8_append(k, v, k8, v8, k_scale, v_scale, frame: int, k_weight=None, rope=None, eps: float = 1e-6,
+                  stream=None) -> None:
+    """New frames into an 8-bit key/value ring of W frames of s tokens (k8, v8:
+    float8_e4m3fn [B, H, W * s, d]; k_scale, v_scale: fp32 [B, H, W, ceil(s / 64)]),
+    the first one being frame number `frame` of the stream, in slot frame mod W.
+
+    k, v: bf16 [B, frames * s, H, d], any strides with contiguous channels.  A
+    k_weight (bf16 or fp32 [d]) norms the keys, rope (tables whose grid is one
+    frame's) rotates them on the way."""
+    device = _current_device(k)
+    B, H, d, s, W = _ring_shape(k8, v8, k_scale, v_scale, device)
+    if k.dim() != 4 or v.shape != k.shape or tuple(k.shape) != (B, k.shape[1], H, d) or k.shape[1] % s:
+        raise ValueError(f"k and v must have shape [{B}, frames * {s}, {H}, {d}]")
+    rows_k, rows_v = _rows_arg("k", k, k_weight, d, device), _rows_arg("v", v, None, d, device)
+    check(ra_cache8_append(_ref(rows_k), _ref(rows_v), B, k.shape[1] // s, d, s, W, frame, _ref(_rope_arg(rope, device)),
+                           eps, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                           _stream_handle(stream)), "ra_cache8_append")
+
+
+def cache8_attention(q, k8, v8, k_scale, v_scale, held: int, key_counts=None, scale: float | None = None, out=None,
+                     lse=None, workspace=None, stream=None):
+    """Attention of q (bf16 [B, H, nq, d], nq >= 1) over the frames in slots 0 ..
+    held - 1 of an 8-bit ring (see cache8_append).  key_counts (int32 [B]) limits
+    each batch element to its first rows; a query without keys gets 0 (lse -inf)."""
+    import torch
+    device = _current_device(q)
+    B, H, d, s, W = _ring_shape(k8, v8, k_scale, v_scale, device)
+    _check_bf16_cuda("q", q)
+    if q.dim() != 4 or tuple(q.shape) != (B, H, q.shape[2], d):
+        raise ValueError(f"q must have shape [{B}, {H}, nq, {d}]")
+    nq = q.shape[2]
+    if key_counts is not None and (key_counts.dtype is not torch.int32 or tuple(key_counts.shape) != (B,)
+                                   or not key_counts.is_contiguous() or key_counts.device != device):
+        raise ValueError(f"key_counts must be a contiguous int32 tensor [{B}] on {device}")
+    if lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (B, H, nq)
+                            or not lse.is_contiguous() or lse.device != device):
+        raise ValueError("lse must be a contiguous fp32 tensor [B, H, nq]")
+    handle = _stream_handle(stream)
+    out = _head_major_out("out", out, (B, H, nq, d), device, stream, handle)
+    if nq == 0:
+        return out
+    need = ctypes.c_size_t()
+    check(ra_cache8_attention_workspace_bytes(B, H, d, nq, s, W, held, ctypes.byref(need)), "ra_cache8_attention")
+    workspace = _workspace(workspace, need.value, device, stream, handle)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    check(ra_cache8_attention(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                              out.data_ptr(), B, H, d, nq, s, W, held,
+                              None if key_counts is None else key_counts.data_ptr(), scale,
+                              None if lse is None else lse.data_ptr(),
+                              None if workspace is None else workspace.data_ptr(), need.value, handle),
+          "ra_cache8_attention")
+    return out
+
+
+class SwcCache8:
+    """Streaming sliding-window causal attention over an 8-bit key/value ring: the
+    window of SwcCache in half its memory, fed with the projections' rows, which
+    are normed and rotated on the way.
+
+    k8, v8, k_scale and v_scale are the ring's buffers (see cache8_append).  Steps
+    must be ordered on one stream, and are refused while it is being captured into a
+    CUDA graph (a replay would repeat one frame number): capture cache8_append and
+    cache8_attention there instead."""
+
+    def __init__(self, B: int, H: int, d: int, s: int, window_frames: int):
+        import torch
+        if min(B, H, s, window_frames) < 1:
+            raise ValueError("B, H, s and window_frames must be >= 1")
+        if d not in (64, 128):
+            raise ValueError(f"head dim {d} is not supported (64 or 128)")
+        self.B, self.H, self.d, self.s, self.W = B, H, d, s, window_frames
+        # zeros: slots not yet filled hold numbers too
+        self.k8, self.v8 = (torch.zeros((B, H, window_frames * s, d), dtype=torch.uint8, device="cuda")
+                            .view(torch.float8_e4m3fn) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.ones((B, H, window_frames, -(-s // CACHE8_BLOCK)), device="cuda")
+                                      for _ in range(2))
+        self.frames_seen = 0
+
+    @property
+    def frames_held(self) -> int:
+        return min(self.frames_seen, self.W)
+
+    @property
+    def info(self) -> dict:
+        return dict(frames_seen=self.frames_seen, frames_held=self.frames_held)
+
+    @property
+    def _ring(self):
+        return self.k8, self.v8, self.k_scale, self.v_scale
+
+    def append(self, k, v, k_weight=None, rope=None, eps: float = 1e-6, stream=None) -> None:
+        """One or more new frames (k, v: bf16 [B, frames * s, H, d]); of more than W
+        the last W are kept."""
+        _refuse_capture(stream)
+        if k.dim() != 4 or v.shape != k.shape or k.shape[1] < self.s or k.shape[1] % self.s:
+            raise ValueError(f"k and v must have shape [{self.B}, frames * {self.s}, {self.H}, {self.d}]")
+        frames = k.shape[1] // self.s
+        skip = max(0, frames - self.W)
+        cache8_append(k[:, skip * self.s:], v[:, skip * self.s:], *self._ring, self.frames_seen + skip, k_weight, rope,
+                      eps, stream)
+        self.frames_seen += frames
+
+    def attend(self, q, out=None, lse=None, scale: float | None = None, workspace=None, stream=None):
+        """Attention of q (bf16 [B, H, nq, d]) over every token of the frames held."""
+        return cache8_attention(q, *self._ring, self.frames_held, None, scale, out, lse, workspace, stream)
+
+    def step(self, q, k, v, q_weight=None, k_weight=None, rope=None, eps: float = 1e-6, out=None, lse=None,
+             scale: float | None = None, stream=None):
+        """Feed the next frame (q, k, v: bf16 [B, s, H, d], the projections' rows);
+        returns its output, bf16 [B, H, s, d]."""
+        _refuse_capture(stream)
+        if tuple(q.shape) != (self.B, self.s, self.H, self.d) or q.shape != k.shape:
+            raise ValueError(f"q, k and v must have shape [{self.B}, {self.s}, {self.H}, {self.d}]")
+        if q_weight is None and rope is None:
+            with _allocating_on(stream, _stream_handle(stream)):
+                q = q.transpose(1, 2).contiguous()
+        else:
+            q, _ = qk_norm_rope(q, None, q_weight, None, rope, self.frames_seen, eps, stream=stream)
+        self.append(k, v, k_weight, rope, eps, stream)
+        return self.attend(q, out, lse, scale, stream=stream)
+
+    def reset(self) -> None:
+        """Forget every frame (the next one is frame 0)."""
+        self.frames_seen = 0
 
 
 class DenseFirstPolicy:

@@ -64,6 +64,40 @@ ra_status attention_fwd_rect(const void* Q, const void* K, const void* V, void* 
                              const unsigned char* flag, int nbq, int nnz, float scale, float* lse,
                              cudaStream_t stream);
 
+// The bytes [lo, hi) of a buffer; empty when lo == hi.
+struct Span {
+    uintptr_t lo, hi;
+};
+
+inline Span span(const void* p, long long bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return p ? Span{a, a + static_cast<uintptr_t>(bytes)} : Span{0, 0};
+}
+
+inline bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Bytes from the first to behind the last element of a strided [B, n, H, d] tensor.
+inline long long extent(long long sb, long long sn, long long sh, int B, int n, int H, int d)
+{
+    return ((B - 1) * sb + (n - 1) * sn + (H - 1) * sh + d) * 2;
+}
+
+struct RopeArgs;
+
+// Check a rope description against n tokens from frame frame0 on and fill the
+// kernels' arguments (no rotation when rope is NULL).
+ra_status rope_args(const ra_rope* rope, int frame0, int n, int d, RopeArgs* out);
+
+// Check one strided [B, n, heads, d] input and return its strides (0 where the
+// dimension has one element).
+ra_status head_rows_args(const char* what, const ra_head_rows* r, int B, int n, int d, long long* sb, long long* sn,
+                         long long* sh);
+
+// Check the 8-bit key/value ring of a call.
+ra_status check_cache8(const void* k8, const void* v8, const float* k_scale, const float* v_scale, int B, int H, int d,
+                       int s, int W);
+
 // Device address of the forward / backward kernels' error word on the current device.
 ra_status device_error_word(int** out);
 
