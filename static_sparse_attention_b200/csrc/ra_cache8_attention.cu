@@ -16,7 +16,7 @@
 #include <cmath>
 #include <cstring>
 
-#include "ra_cache8.cuh"
+#include "ra_cache8_attention.cuh"
 #include "ra_internal.h"
 
 namespace ra {
@@ -25,29 +25,6 @@ namespace {
 constexpr int ROWS = 16;   // queries of a block
 constexpr int WARPS = 4;
 constexpr int GROUP = 16;  // keys that a warp takes at a time
-constexpr float LN2 = 0.69314718055994530942f;
-
-struct AttnParams {
-    const __nv_bfloat16* Q;  // [B, H, nq, d]
-    const uint8_t* k8;       // [B, H, W * s, d]
-    const uint8_t* v8;
-    const float* k_scale;    // [B, H, W, blocks]
-    const float* v_scale;
-    const int* counts;       // [B] keys of each batch element, or null: nk
-    __nv_bfloat16* O;        // [B, H, nq, d]
-    float* lse;              // [B, H, nq] or null
-    float* part_o;           // [B, H, nq, splits, d], when splits > 1
-    float2* part_ml;         // [B, H, nq, splits]: maximum (base 2) and sum
-    int H, nq, s, W, blocks, nk;
-    int q_tiles, splits, chunk;  // keys of a split
-    float scale_log2;
-};
-
-__device__ __forceinline__ int key_count(const AttnParams& p, int b)
-{
-    return p.counts ? min(max(p.counts[b], 0), p.nk) : p.nk;
-}
-
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -116,8 +93,7 @@ __device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, lon
     const int key = key0 + (lane & 15);
     g.scale = 0.f;
     if (key < end) {
-        const int slot = key / p.s, blk = (key - slot * p.s) / CACHE8_BLOCK;
-        const long long at = (bh * p.W + slot) * p.blocks + blk;
+        const long long at = scale_index(p, bh, key);
         g.scale = lane < 16 ? p.k_scale[at] : p.v_scale[at];
     }
 }
@@ -344,12 +320,19 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
         p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-// How the keys are split over blocks: enough blocks for every SM, at least
-// MIN_CHUNK keys each.
+// How the work is cut.  Few queries: ranges of at least MIN_CHUNK keys, enough
+// blocks for every SM.  Many: the number of ranges with the least estimated time,
+// counted in steps of 64 keys of the 256-query kernel (one block an SM).
 constexpr int MIN_CHUNK = 256;
-constexpr int WANT_BLOCKS = 148 * 8;
+constexpr int SMS = 148;
+constexpr int WANT_BLOCKS = SMS * 8;
+constexpr int TILES_MIN_QUERIES = 33;  // more queries than this go to the many-query kernel
+constexpr double STEP_US = 0.9;        // a step of 64 keys of 256 queries
+constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
+constexpr double JOIN_BYTES_PER_US = 5e6;
 
 struct Plan {
+    bool many;
     int q_tiles, splits, chunk;
     size_t bytes;
 };
@@ -357,16 +340,34 @@ struct Plan {
 Plan plan_of(int B, int H, int d, int nq, int nk)
 {
     Plan pl;
-    pl.q_tiles = (nq + ROWS - 1) / ROWS;
+    pl.many = nq >= TILES_MIN_QUERIES;
+    const int rows = pl.many ? 256 : ROWS, unit = pl.many ? 64 : GROUP * WARPS;
+    pl.q_tiles = (nq + rows - 1) / rows;
     const long long tiles = static_cast<long long>(pl.q_tiles) * H * B;
-    long long splits = (WANT_BLOCKS + tiles - 1) / tiles;
-    const long long most = (static_cast<long long>(nk) + MIN_CHUNK - 1) / MIN_CHUNK;
-    splits = splits < most ? splits : most;
-    splits = splits < 1 ? 1 : splits;
-    pl.chunk = static_cast<int>((nk + splits - 1) / splits);
-    pl.chunk = (pl.chunk + GROUP * WARPS - 1) / (GROUP * WARPS) * (GROUP * WARPS);
-    pl.chunk = pl.chunk < GROUP * WARPS ? GROUP * WARPS : pl.chunk;
-    pl.splits = (nk + pl.chunk - 1) / pl.chunk;
+    long long splits = 1;
+    if (pl.many) {
+        const long long steps = (static_cast<long long>(nk) + unit - 1) / unit;
+        const double part = static_cast<double>(B) * H * nq * (d + 2) * 4 * 2 / JOIN_BYTES_PER_US / STEP_US;
+        double best = 0;
+        for (long long k = 1; k <= 32 && k * 4 <= (steps > 4 ? steps : 4); ++k) {
+            const double rounds = static_cast<double>((tiles * k + SMS - 1) / SMS);
+            const double cost = rounds * (static_cast<double>((steps + k - 1) / k) + START_STEPS) +
+                                (k > 1 ? part * static_cast<double>(k) + 5 : 0);
+            if (k == 1 || cost < best) {
+                best = cost;
+                splits = k;
+            }
+        }
+    } else {
+        splits = (WANT_BLOCKS + tiles - 1) / tiles;
+        const long long most = (static_cast<long long>(nk) + MIN_CHUNK - 1) / MIN_CHUNK;
+        splits = splits < most ? splits : most;
+        splits = splits < 1 ? 1 : splits;
+    }
+    const long long chunk = (nk + splits - 1) / splits;
+    pl.chunk = static_cast<int>((chunk + unit - 1) / unit * unit);
+    pl.chunk = pl.chunk < unit ? unit : pl.chunk;
+    pl.splits = static_cast<int>((static_cast<long long>(nk) + pl.chunk - 1) / pl.chunk);
     pl.splits = pl.splits < 1 ? 1 : pl.splits;
     pl.bytes = pl.splits == 1 ? 0 : static_cast<size_t>(B) * H * nq * pl.splits * (d + 2) * sizeof(float);
     return pl;
@@ -457,6 +458,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     p.W = window_frames;
     p.blocks = blocks;
     p.nk = held * s;
+    p.per_s = s == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((1ULL << 32) / static_cast<unsigned>(s));
     p.q_tiles = pl.q_tiles;
     p.splits = pl.splits;
     p.chunk = pl.chunk;
@@ -466,12 +468,18 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
         p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(rows) * pl.splits * d);
     }
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
-    if (d == 64)
-        cache8_rows_kernel<64><<<grid, WARPS * 32, 0, cs>>>(p);
-    else
-        cache8_rows_kernel<128><<<grid, WARPS * 32, 0, cs>>>(p);
-    RA_CUDA_TRY(cudaGetLastError());
+    if (pl.many) {
+        p.timeout_ns = wait_timeout_ns();
+        if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, cs)) != RA_OK)
+            return st;
+    } else {
+        const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
+        if (d == 64)
+            cache8_rows_kernel<64><<<grid, WARPS * 32, 0, cs>>>(p);
+        else
+            cache8_rows_kernel<128><<<grid, WARPS * 32, 0, cs>>>(p);
+        RA_CUDA_TRY(cudaGetLastError());
+    }
     if (pl.splits == 1)
         return RA_OK;
     const unsigned joins = static_cast<unsigned>((rows + 3) / 4);

@@ -1,0 +1,553 @@
+// ra_cache8_tiles.cu -- attention of many queries over the 8-bit key/value ring
+// on the tensor cores (tcgen05, accumulators in TMEM).
+//
+// One CTA per (head, 256 queries, range of keys), one CTA per SM, keys in steps
+// of 64.  Four warpgroups in fixed roles:
+//   warps 0-3, 4-7  softmax of query tile 0 and 1 (128 rows each): thread t of the
+//                   group owns row t (TMEM lane t); per step reads S, keeps the
+//                   running maximum and sum, writes P (bf16) back over S; at the end
+//                   the epilogue.
+//   warps 8-11      convert: the codes of a step's 64 keys and values come from
+//                   memory to registers one step ahead (16 bytes a thread and row,
+//                   the rows of a step are contiguous), become code * scale in bf16
+//                   -- exactly, see ra_cache8.cuh -- and go into a ring of shared
+//                   memory stages in the MMA's 128-byte swizzle.
+//   warp 12         (13-15 only make up its warpgroup) MMA: allocates TMEM; one elected lane issues, for both tiles,
+//                   S_h = Q K_h^T (N = 64) into S buffer h % 2 and O += P_h V_h, in
+//                   the order S_0, S_1, PV_0, S_2, PV_1, ...
+// Two query tiles share one conversion: per step it costs about 5.5 integer and
+// multiply instructions for two codes, 1400 warp instructions for 64 keys of 128
+// channels, against 2900 for the softmax of 2 x 128 x 64 scores and 1280 clocks of
+// the tensor pipe; with one tile a CTA it would not hide behind them.
+//
+// A word of four codes is turned into two pairs, channels (0, 2) and (1, 3), which
+// saves the byte permutes.  So channels lie in the order 0, 2, 1, 3 within every
+// four in shared memory: Q is stored in the same order (S does not depend on it),
+// and the epilogue puts O's columns, which follow V's, back.
+//
+// S_{h+2} overwrites the TMEM columns whose P the P V of step h reads.  The PTX
+// ISA executes two tcgen05 operations of a thread in order for the pairs that it
+// lists as pipelined; MMA -> shift and shift -> MMA are such pairs for any two of
+// the same cta_group, so a tcgen05.shift of columns that S_{h+2} overwrites anyway
+// orders it behind that P V.  O is rescaled only after the step before has
+// completed.  Every wait is bounded (ra_sm100.cuh).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "ra_cache8_attention.cuh"
+#include "ra_internal.h"
+#include "ra_sm100.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int STEP = 64;           // keys of a step
+constexpr int TILE_ROWS = 128;     // queries of a tile
+constexpr int THREADS = 512;
+constexpr int CONVERT_WARP = 8, MMA_WARP = 12;
+// Registers a thread of each warpgroup keeps of the 128 that the block is launched
+// with: the softmax holds 64 scores, P and its sums.
+constexpr int SOFTMAX_REGS = 160, CONVERT_REGS = 112, MMA_REGS = 72;
+static_assert(2 * SOFTMAX_REGS + CONVERT_REGS + MMA_REGS <= 4 * 128, "the split draws on the block's own registers");
+constexpr uint32_t TMEM_COLS = 512;
+// TMEM columns of a tile: S / P buffers 0 and 1 (64 fp32 columns each), then O.
+__host__ __device__ constexpr uint32_t tile_col(int t) { return 256u * static_cast<uint32_t>(t); }
+__host__ __device__ constexpr uint32_t s_col(int t, int buf) { return tile_col(t) + 64u * static_cast<uint32_t>(buf); }
+__host__ __device__ constexpr uint32_t o_col(int t) { return tile_col(t) + 128u; }
+// The running maximum (base 2) is raised only when a step exceeds it by more: P
+// stays below 2^8, which fp32 and bf16 hold as precisely as values below 1.
+constexpr float RAISE = 8.0f;
+
+enum : int {
+    SITE_EMPTY = 60, SITE_K_FULL, SITE_V_FULL, SITE_P_FULL, SITE_S_FULL, SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN
+};
+
+template <int D>
+struct Layout {
+    static constexpr int CHUNKS = D / 64;                       // 128-byte swizzle atoms across d
+    static constexpr int Q_CHUNK = TILE_ROWS * 128;             // bytes of 128 rows x 64 channels
+    static constexpr int Q_TILE = CHUNKS * Q_CHUNK;
+    static constexpr int KV_CHUNK = STEP * 128;
+    static constexpr int KV_TILE = CHUNKS * KV_CHUNK;           // K or V of a step
+    static constexpr int STAGES = 4;
+    static constexpr int K_OFF = 2 * Q_TILE;
+    static constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
+    static constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
+    static constexpr int SMEM = BAR_OFF + 256;
+};
+
+enum : int {
+    B_K_FULL = 0,                // + stage
+    B_V_FULL = 4,                // + stage
+    B_EMPTY = 8,                 // + stage
+    B_S_FULL = 12,               // + 2 * tile + buffer
+    B_P_FULL = 16,               // + 2 * tile + buffer
+    B_PV_DONE = 20,              // + tile
+    B_O_FINAL = 22,
+    B_COUNT = 23
+};
+
+// ---- packed fp32 pairs -------------------------------------------------------
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// p = 2^(s * c - m) of 32 columns, packed to bf16, summed into four pairs of
+// accumulators; MAX also tracks the largest s.
+template <bool MAX>
+__device__ __forceinline__ void exp_columns(const uint32_t (&s)[32], float c, float negm, uint64_t (&sum)[4],
+                                            float (&top)[4], uint32_t (&p)[16])
+{
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+        const float s0 = __uint_as_float(s[e]), s1 = __uint_as_float(s[e + 1]);
+        if (MAX)
+            top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], s0, s1);
+        float x0, x1;
+        unpair(pair_fma(pair(s0, s1), pair(c, c), pair(negm, negm)), x0, x1);
+        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+        sum[(e >> 1) & 3] = pair_add(sum[(e >> 1) & 3], pair(p0, p1));
+        p[e >> 1] = pack_bf16(p0, p1);
+    }
+}
+
+// Four codes to bf16 code * factor: channels (0, 2) in x, (1, 3) in y.
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t factor, uint32_t& x, uint32_t& y)
+{
+    x = mul_bf16x2(e4m3x2_small(w << 8), factor);
+    y = mul_bf16x2(e4m3x2_small(w), factor);
+}
+
+// The codes and scales of a step's rows that a convert thread takes: 16 bytes of
+// row first + i * ROW_STEP for K and V each.
+template <int D>
+struct Piece {
+    static constexpr int PER_ROW = D / 16;             // threads a row
+    static constexpr int ROW_STEP = 128 / PER_ROW;
+    static constexpr int N = STEP / ROW_STEP;
+    uint4 code[N];
+    float scale[N];
+};
+
+template <int D>
+__device__ __forceinline__ void load_piece(Piece<D>& x, const uint8_t* codes, const float* scales, const AttnParams& p,
+                                           long long bh, int key0, int end, int thread)
+{
+    using P = Piece<D>;
+    const int part = thread % P::PER_ROW, first = thread / P::PER_ROW;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) {
+        const int key = key0 + first + i * P::ROW_STEP;
+        x.code[i] = make_uint4(0, 0, 0, 0);
+        x.scale[i] = 0.f;
+        if (key < end) {
+            x.code[i] = __ldg(reinterpret_cast<const uint4*>(codes + (bh * p.W * p.s + key) * D + part * 16));
+            x.scale[i] = __ldg(scales + scale_index(p, bh, key));
+        }
+    }
+}
+
+// Convert a step's rows of K or V into a stage.
+template <int D>
+__device__ __forceinline__ void store_piece(const Piece<D>& x, uint8_t* stage, int thread)
+{
+    using P = Piece<D>;
+    const int part = thread % P::PER_ROW, first = thread / P::PER_ROW;
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) {
+        const int row = first + i * P::ROW_STEP;
+        const CodeScale cs = code_scale(x.scale[i]);
+        const uint32_t f = cs.first | (cs.first << 16);
+        const uint32_t w[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+        uint32_t out[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            codes4(w[j], f, out[2 * j], out[2 * j + 1]);
+        if (cs.second != 0x3F80u) {
+            const uint32_t f2 = cs.second | (cs.second << 16);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                out[j] = mul_bf16x2(out[j], f2);
+        }
+        // 16-byte units 2 part and 2 part + 1 of the row.  With eight threads a row
+        // the upper four store theirs in the other order, so that the eight of a
+        // store fall on different banks.
+        const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
+        const int swap = D == 128 ? part >> 2 : 0;
+        uint8_t* at = stage + (part >> 2) * Layout<D>::KV_CHUNK + row * 128;
+        const int unit = 2 * (part & 3);
+        *reinterpret_cast<uint4*>(at + (((unit + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(at + (((unit + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+    }
+}
+
+template <int REGS>
+__device__ __forceinline__ void shed_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnParams p)
+{
+    using L = Layout<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t bars = sbase + L::BAR_OFF;
+    auto bar = [&](int i) -> uint32_t { return bars + 8u * static_cast<uint32_t>(i); };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::BAR_OFF + 8 * B_COUNT);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::BAR_OFF + 8 * B_COUNT + 4);
+
+    const int warp = threadIdx.x >> 5;
+    const int split = static_cast<int>(blockIdx.x) % p.splits, q_tile = static_cast<int>(blockIdx.x) / p.splits;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const long long bh = static_cast<long long>(b) * p.H + h;
+    const int count = key_count(p, b);
+    const int begin = split * p.chunk;
+    if (p.splits > 1 && begin >= count)
+        return;  // the join does not read this split
+    const int end = min(begin + p.chunk, count);
+    const int q0 = q_tile * 2 * TILE_ROWS;
+    const int tiles = p.nq - q0 > TILE_ROWS ? 2 : 1;
+    WaitCtl wc{abort_flag, p.err, p.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        *abort_flag = *reinterpret_cast<volatile int*>(p.err) != 0 ? 1 : 0;
+        if (sbase & 1023u)  // the swizzled tiles need 1024-byte alignment: record it, run nothing
+            report_timeout(wc, SITE_SMEM_ALIGN);
+        for (int i = 0; i < B_COUNT; ++i)
+            mbar_init(bar(i), i < B_EMPTY || (i >= B_P_FULL && i < B_PV_DONE) ? 128u : 1u);
+        fence_barrier_init();
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(smem_addr(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    // Q, zeros behind the last query, in the order of channels that K has
+    for (int i = threadIdx.x; i < tiles * TILE_ROWS * (D / 8); i += THREADS) {
+        const int row = i / (D / 8), unit = i % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (q0 + row < p.nq)
+            v = *reinterpret_cast<const uint4*>(p.Q + (bh * p.nq + q0 + row) * D + unit * 8);
+        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
+                       __byte_perm(v.z, v.w, 0x7632));
+        uint8_t* at = smem + (row / TILE_ROWS) * L::Q_TILE + (unit / 8) * L::Q_CHUNK + (row % TILE_ROWS) * 128;
+        *reinterpret_cast<uint4*>(at + (((unit % 8) ^ (row & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool skip = *abort_flag != 0;  // an earlier kernel gave up: do nothing
+    const int n = skip || end <= begin ? 0 : (end - begin + STEP - 1) / STEP;
+
+    if (warp >= MMA_WARP) {
+        // ----------------------------------------------------------------- MMA
+        shed_registers<MMA_REGS>();
+        if (warp == MMA_WARP && n > 0) {
+            const bool leader = elect_one();
+            constexpr uint32_t idesc_s = idesc_bf16_f32(TILE_ROWS, STEP, 0, 0);
+            constexpr uint32_t idesc_pv = idesc_bf16_f32(TILE_ROWS, D, 0, 1);
+            const uint64_t q_desc = smem_desc_sw128(sbase, 16, 1024);
+            const uint64_t k_desc = smem_desc_sw128(sbase + L::K_OFF, 16, 1024);
+            const uint64_t v_desc = smem_desc_sw128(sbase + L::V_OFF, L::KV_CHUNK, 1024);  // V as MN-major B
+            auto wait_all = [&](uint32_t bb, uint32_t parity, int site) {
+                return __all_sync(0xFFFFFFFFu, mbar_wait(bb, parity, wc, site)) != 0;
+            };
+            bool ok = true;
+            for (int hh = 0; ok && hh <= n; ++hh) {
+                if (hh < n) {
+                    const int st = hh % L::STAGES;
+                    if (!(ok = wait_all(bar(B_K_FULL + st), (hh / L::STAGES) & 1, SITE_K_FULL)))
+                        break;
+                    tc_fence_after();
+                    const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
+                    for (int t = 0; t < tiles; ++t) {
+                        // behind the P V of step hh - 2, which reads this buffer (see the header)
+                        if (hh >= 2 && leader)
+                            tmem_shift_down(tmem + s_col(t, hh & 1));
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint64_t ad =
+                                desc_add(q_desc, t * L::Q_TILE + (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
+                            const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
+                            mma_ss(leader, tmem + s_col(t, hh & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+                        }
+                        if (leader)
+                            mma_commit(bar(B_S_FULL + 2 * t + (hh & 1)));
+                    }
+                }
+                if (hh >= 1) {
+                    const int j = hh - 1, st = j % L::STAGES, buf = j & 1;
+                    const uint64_t vd = desc_add(v_desc, st * L::KV_TILE);
+                    for (int t = 0; t < tiles; ++t) {
+                        if (t == 0 && !(ok = wait_all(bar(B_V_FULL + st), (j / L::STAGES) & 1, SITE_V_FULL)))
+                            break;
+                        if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (j >> 1) & 1, SITE_P_FULL)))
+                            break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < STEP / 16; ++kk)
+                            mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048),
+                                   idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
+                        if (leader)
+                            mma_commit(bar(B_PV_DONE + t));
+                    }
+                    if (ok && leader)
+                        mma_commit(bar(B_EMPTY + st));
+                }
+            }
+            if (leader)
+                mma_commit(bar(B_O_FINAL));
+            // Every MMA issued by the elected lane has completed once O_FINAL fires.
+            drain_wait(bar(B_O_FINAL), 0, p.timeout_ns);
+        }
+    } else if (warp >= CONVERT_WARP) {
+        // ------------------------------------------------------------- convert
+        shed_registers<CONVERT_REGS>();
+        const int thread = threadIdx.x - CONVERT_WARP * 32;
+        Piece<D> k, v;
+        if (n > 0) {
+            load_piece<D>(k, p.k8, p.k_scale, p, bh, begin, end, thread);
+            load_piece<D>(v, p.v8, p.v_scale, p, bh, begin, end, thread);
+        }
+        for (int hh = 0; hh < n; ++hh) {
+            const int st = hh % L::STAGES;
+            if (hh >= L::STAGES &&
+                !__all_sync(0xFFFFFFFFu, mbar_wait(bar(B_EMPTY + st), ((hh / L::STAGES) - 1) & 1, wc, SITE_EMPTY)))
+                break;
+            const int next = begin + (hh + 1) * STEP;
+            const Piece<D> k_now = k;
+            if (hh + 1 < n)
+                load_piece<D>(k, p.k8, p.k_scale, p, bh, next, end, thread);
+            store_piece<D>(k_now, smem + L::K_OFF + st * L::KV_TILE, thread);
+            fence_proxy_async_smem();
+            mbar_arrive(bar(B_K_FULL + st));
+            const Piece<D> v_now = v;
+            if (hh + 1 < n)
+                load_piece<D>(v, p.v8, p.v_scale, p, bh, next, end, thread);
+            store_piece<D>(v_now, smem + L::V_OFF + st * L::KV_TILE, thread);
+            fence_proxy_async_smem();
+            mbar_arrive(bar(B_V_FULL + st));
+        }
+    } else if (warp < 4 * tiles) {
+        // ------------------------------------------------------------- softmax
+        take_registers<SOFTMAX_REGS>();
+        const int t = warp >> 2;
+        const int row = q0 + t * TILE_ROWS + (threadIdx.x & 127);
+        const bool row_valid = row < p.nq;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const float c = p.scale_log2;
+        float m_run = -INFINITY, l_run = 0.f;
+        bool ok = true;
+        for (int hh = 0; hh < n; ++hh) {
+            const uint32_t col = s_col(t, hh & 1);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_S_FULL + 2 * t + (hh & 1)), (hh >> 1) & 1, wc, SITE_S_FULL));
+            if (!ok)
+                break;
+            tc_fence_after();
+            uint32_t s[2][32];
+            tmem_ld32(lanes + col, s[0]);
+            tmem_ld32(lanes + col + 32, s[1]);
+            tmem_wait_ld();
+            const int valid = end - (begin + hh * STEP);  // keys of this step
+            if (valid < STEP) {
+#pragma unroll
+                for (int e = 0; e < STEP; ++e)
+                    if (e >= valid)
+                        s[e / 32][e % 32] = __float_as_uint(-INFINITY);
+            }
+            auto exp_pass = [&](float m_use, bool with_max, float& top) -> float {
+                uint64_t sum[4] = {0, 0, 0, 0};
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t pk[16];
+                    if (with_max)
+                        exp_columns<true>(s[k], c, -m_use, sum, mx, pk);
+                    else
+                        exp_columns<false>(s[k], c, -m_use, sum, mx, pk);
+                    tmem_st16(lanes + col + k * 16, pk);
+                }
+                top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float lo, hi;
+                unpair(pair_add(pair_add(sum[0], sum[1]), pair_add(sum[2], sum[3])), lo, hi);
+                return lo + hi;
+            };
+            // Raise the running maximum (for the whole warp) and rescale O and l, once
+            // the P V of the step before has completed.
+            bool raised = true;
+            auto raise_max = [&](float m_step) {
+                const float m_new = fmaxf(m_run, m_step);
+                const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_run - m_new);
+                if (hh > 0) {
+                    raised = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_PV_DONE + t), (hh - 1) & 1, wc, SITE_PV_DONE));
+                    if (!raised)
+                        return;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + o_col(t) + k * 32, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(lanes + o_col(t) + k * 32, o);
+                    }
+                }
+                l_run *= alpha;
+                m_run = m_new;
+            };
+            float sum, top;
+            if (__any_sync(0xFFFFFFFFu, m_run == -INFINITY)) {
+                // no reference maximum yet in this warp: the maximum first
+                float mx[8];
+#pragma unroll
+                for (int a = 0; a < 8; ++a)
+                    mx[a] = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < STEP; ++e)
+                    mx[e % 8] = fmaxf(mx[e % 8], __uint_as_float(s[e / 32][e % 32]));
+#pragma unroll
+                for (int w = 4; w >= 1; w /= 2)
+#pragma unroll
+                    for (int a = 0; a < w; ++a)
+                        mx[a] = fmaxf(mx[a], mx[a + w]);
+                const float m_step = mx[0] * c;  // c > 0
+                if (__any_sync(0xFFFFFFFFu, m_step > m_run + RAISE))
+                    raise_max(m_step);
+                sum = exp_pass(m_run == -INFINITY ? 0.f : m_run, false, top);
+            } else {
+                // one pass against the running maximum; redone in the rare step that exceeds it by more than RAISE
+                sum = exp_pass(m_run, true, top);
+                const float m_step = top * c;
+                if (__any_sync(0xFFFFFFFFu, m_step > m_run + RAISE)) {
+                    raise_max(m_step);
+                    sum = exp_pass(m_run, false, top);
+                }
+            }
+            if (!(ok = raised))
+                break;
+            l_run += sum;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(bar(B_P_FULL + 2 * t + (hh & 1)));
+        }
+
+        // ------------------------------------------------------------ epilogue
+        if (n > 0 && ok)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_O_FINAL), 0, wc, SITE_O_FINAL));
+        tc_fence_after();
+        if (ok && !*abort_flag) {
+            const long long at = bh * p.nq + row;
+            const float f = p.splits > 1 ? 1.f : (l_run == 0.f ? 0.f : 1.f / l_run);
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(lanes + o_col(t) + k * 32, o);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0u;
+                }
+                float x[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {  // columns 1 and 2 of every four hold channels 2 and 1
+                    const int from = (e & 3) == 1 ? e + 1 : ((e & 3) == 2 ? e - 1 : e);
+                    x[e] = __uint_as_float(o[from]) * f;
+                }
+                if (!row_valid)
+                    continue;
+                if (p.splits > 1) {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + (at * p.splits + split) * D + k * 32);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        dst[u] = make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+                } else {
+                    uint4* dst = reinterpret_cast<uint4*>(p.O + at * D + k * 32);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        dst[u] = make_uint4(pack_bf16(x[8 * u], x[8 * u + 1]), pack_bf16(x[8 * u + 2], x[8 * u + 3]),
+                                            pack_bf16(x[8 * u + 4], x[8 * u + 5]),
+                                            pack_bf16(x[8 * u + 6], x[8 * u + 7]));
+                }
+            }
+            if (row_valid) {
+                if (p.splits > 1)
+                    p.part_ml[at * p.splits + split] = make_float2(m_run, l_run);
+                else if (p.lse)
+                    p.lse[at] = l_run == 0.f ? -INFINITY : (m_run + log2f(l_run)) * LN2;
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == MMA_WARP) {
+        __syncwarp();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <int D>
+ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
+{
+    static std::once_flag once;
+    static cudaError_t err = cudaSuccess;
+    std::call_once(once, [] {
+        err = cudaFuncSetAttribute(cache8_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   Layout<D>::SMEM);
+    });
+    if (err != cudaSuccess)
+        return cuda_fail(err, "cudaFuncSetAttribute(cache8_tiles_kernel)");
+    const dim3 grid(static_cast<unsigned>(p.q_tiles) * p.splits, p.H, B);
+    cache8_tiles_kernel<D><<<grid, THREADS, Layout<D>::SMEM, cs>>>(p);
+    return cuda_fail(cudaGetLastError(), "cache8_tiles_kernel launch");
+}
+
+}  // namespace
+
+ra_status cache8_tiles(const AttnParams& p, int B, int d, cudaStream_t cs)
+{
+    return d == 64 ? launch<64>(p, B, cs) : launch<128>(p, B, cs);
+}
+
+}  // namespace ra
