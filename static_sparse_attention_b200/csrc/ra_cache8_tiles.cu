@@ -7,12 +7,13 @@
 //                   group owns row t (TMEM lane t); per step reads S, keeps the
 //                   running maximum and sum, writes P (bf16) back over S; at the end
 //                   the epilogue.
-//   warps 8-11      convert: the codes of a step's 64 keys and values come from
-//                   memory to registers one step ahead (16 bytes a thread and row,
-//                   the rows of a step are contiguous), become code * scale in bf16
-//                   -- exactly, see ra_cache8.cuh -- and go into a ring of shared
-//                   memory stages in the MMA's 128-byte swizzle.
-//   warp 12         (13-15 only make up its warpgroup) MMA: allocates TMEM; one elected lane issues, for both tiles,
+//   warp 13         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
+//                   are contiguous) into a ring of shared memory, RAW steps ahead; its
+//                   lanes turn the rows' scales into the factors of the conversion.
+//   warps 8-11      convert: codes become code * scale in bf16 -- exactly, see
+//                   ra_cache8.cuh -- in the MMA's 128-byte swizzle, in a ring of K
+//                   stages and one of V stages.
+//   warp 12         MMA: allocates TMEM; one elected lane issues, for both tiles,
 //                   S_h = Q K_h^T (N = 64) into S buffer h % 2 and O += P_h V_h, in
 //                   the order S_0, S_1, PV_0, S_2, PV_1, ...
 // Two query tiles share one conversion: per step it costs about 5.5 integer and
@@ -31,6 +32,14 @@
 // the same cta_group, so a tcgen05.shift of columns that S_{h+2} overwrites anyway
 // orders it behind that P V.  O is rescaled only after the step before has
 // completed.  Every wait is bounded (ra_sm100.cuh).
+//
+// The convert warps write K and V through the generic proxy and the MMA reads them
+// through the async proxy: the proxy fence between the two stands in the MMA warp,
+// behind its wait for the writers' barrier.
+//
+// With the codes fetched by the convert warps' own loads, two steps ahead, a step
+// took 2350 clocks (1.11 ms for 1560 queries, 24960 keys, 40 heads of 128): they
+// waited for their loads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -47,7 +56,7 @@ namespace {
 constexpr int STEP = 64;           // keys of a step
 constexpr int TILE_ROWS = 128;     // queries of a tile
 constexpr int THREADS = 512;
-constexpr int CONVERT_WARP = 8, MMA_WARP = 12;
+constexpr int CONVERT_WARP = 8, MMA_WARP = 12, FETCH_WARP = 13;
 // Registers a thread of each warpgroup keeps of the 128 that the block is launched
 // with: the softmax holds 64 scores, P and its sums.
 constexpr int SOFTMAX_REGS = 160, CONVERT_REGS = 112, MMA_REGS = 72;
@@ -62,7 +71,8 @@ __host__ __device__ constexpr uint32_t o_col(int t) { return tile_col(t) + 128u;
 constexpr float RAISE = 8.0f;
 
 enum : int {
-    SITE_EMPTY = 60, SITE_K_FULL, SITE_V_FULL, SITE_P_FULL, SITE_S_FULL, SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN
+    SITE_RAW_EMPTY = 60, SITE_RAW_FULL, SITE_K_EMPTY, SITE_V_EMPTY, SITE_K_FULL, SITE_V_FULL, SITE_P_FULL, SITE_S_FULL,
+    SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN
 };
 
 template <int D>
@@ -72,23 +82,50 @@ struct Layout {
     static constexpr int Q_TILE = CHUNKS * Q_CHUNK;
     static constexpr int KV_CHUNK = STEP * 128;
     static constexpr int KV_TILE = CHUNKS * KV_CHUNK;           // K or V of a step
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = 3;                            // of K, and of V
+    static constexpr int RAW = 4;                               // steps of codes
+    static constexpr int RAW_TILE = STEP * D;                   // bytes of K's or V's codes of a step
     static constexpr int K_OFF = 2 * Q_TILE;
     static constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
-    static constexpr int BAR_OFF = V_OFF + STAGES * KV_TILE;
+    static constexpr int RAW_OFF = V_OFF + STAGES * KV_TILE;    // [RAW][K, V]
+    static constexpr int FACTOR_OFF = RAW_OFF + RAW * 2 * RAW_TILE;
+    static constexpr int FACTORS = 2 * STEP + 4;                // words: of K's rows, of V's rows, the TWO flag
+    static constexpr int BAR_OFF = FACTOR_OFF + RAW * FACTORS * 4;
     static constexpr int SMEM = BAR_OFF + 256;
+    static_assert(SMEM <= 227 * 1024, "one block's shared memory");
 };
 
 enum : int {
-    B_K_FULL = 0,                // + stage
-    B_V_FULL = 4,                // + stage
-    B_EMPTY = 8,                 // + stage
-    B_S_FULL = 12,               // + 2 * tile + buffer
-    B_P_FULL = 16,               // + 2 * tile + buffer
-    B_PV_DONE = 20,              // + tile
-    B_O_FINAL = 22,
-    B_COUNT = 23
+    B_K_FULL = 0,      // + stage
+    B_V_FULL = 3,      // + stage
+    B_K_EMPTY = 6,     // + stage
+    B_V_EMPTY = 9,     // + stage
+    B_RAW_FULL = 12,   // + raw stage
+    B_RAW_EMPTY = 16,  // + raw stage
+    B_S_FULL = 20,     // + 2 * tile + buffer
+    B_P_FULL = 24,     // + 2 * tile + buffer
+    B_PV_DONE = 28,    // + tile
+    B_O_FINAL = 30,
+    B_COUNT = 31
 };
+constexpr int CONVERT_WARPS = 4;
+
+// Arrivals that complete a phase of barrier i: the convert warps, the threads of a
+// softmax warpgroup, or one thread (the MMA's commits, the fetch).
+__host__ __device__ constexpr uint32_t arrivals(int i)
+{
+    return i < B_K_EMPTY || (i >= B_RAW_EMPTY && i < B_S_FULL) ? CONVERT_WARPS
+           : i >= B_P_FULL && i < B_PV_DONE                    ? 128u
+                                                               : 1u;
+}
+
+// Contiguous copy of `bytes` (a multiple of 16) into shared memory, completing on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
 
 // ---- packed fp32 pairs -------------------------------------------------------
 __device__ __forceinline__ uint64_t pair(float lo, float hi)
@@ -146,66 +183,48 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t factor, uint32_t& x,
     y = mul_bf16x2(e4m3x2_small(w), factor);
 }
 
-// The codes and scales of a step's rows that a convert thread takes: 16 bytes of
-// row first + i * ROW_STEP for K and V each.
+// How the convert threads share a step's rows: 16 codes a thread, rows `row` and
+// every ROW_STEP behind it.
 template <int D>
-struct Piece {
-    static constexpr int PER_ROW = D / 16;             // threads a row
-    static constexpr int ROW_STEP = 128 / PER_ROW;
+struct Codes {
+    static constexpr int PER_ROW = D / 16;  // threads a row
+    static constexpr int ROW_STEP = CONVERT_WARPS * 32 / PER_ROW;
     static constexpr int N = STEP / ROW_STEP;
-    uint4 code[N];
-    float scale[N];
 };
 
-template <int D>
-__device__ __forceinline__ void load_piece(Piece<D>& x, const uint8_t* codes, const float* scales, const AttnParams& p,
-                                           long long bh, int key0, int end, int thread)
+// Convert a step's codes of K or V into a stage.  TWO: some scale of the step needs
+// its second factor.
+template <int D, bool TWO>
+__device__ __forceinline__ void convert(const uint8_t* raw, const uint32_t* factors, uint8_t* stage, int row, int part)
 {
-    using P = Piece<D>;
-    const int part = thread % P::PER_ROW, first = thread / P::PER_ROW;
-#pragma unroll
-    for (int i = 0; i < P::N; ++i) {
-        const int key = key0 + first + i * P::ROW_STEP;
-        x.code[i] = make_uint4(0, 0, 0, 0);
-        x.scale[i] = 0.f;
-        if (key < end) {
-            x.code[i] = __ldg(reinterpret_cast<const uint4*>(codes + (bh * p.W * p.s + key) * D + part * 16));
-            x.scale[i] = __ldg(scales + scale_index(p, bh, key));
-        }
-    }
-}
-
-// Convert a step's rows of K or V into a stage.
-template <int D>
-__device__ __forceinline__ void store_piece(const Piece<D>& x, uint8_t* stage, int thread)
-{
-    using P = Piece<D>;
-    const int part = thread % P::PER_ROW, first = thread / P::PER_ROW;
-#pragma unroll
-    for (int i = 0; i < P::N; ++i) {
-        const int row = first + i * P::ROW_STEP;
-        const CodeScale cs = code_scale(x.scale[i]);
-        const uint32_t f = cs.first | (cs.first << 16);
-        const uint32_t w[4] = {x.code[i].x, x.code[i].y, x.code[i].z, x.code[i].w};
+    using C = Codes<D>;
+    // 16-byte units 2 part and 2 part + 1 of the row.  With eight threads a row the
+    // upper four store theirs in the other order, so that the eight of a store fall
+    // on different banks.  row and row + i * ROW_STEP have the same swizzle.
+    static_assert(C::ROW_STEP % 8 == 0, "one swizzle for all rows of a thread");
+    const int swap = D == 128 ? part >> 2 : 0;
+    uint8_t* base = stage + (part >> 2) * Layout<D>::KV_CHUNK + row * 128;
+    uint8_t* at0 = base + (((2 * (part & 3) + swap) ^ (row & 7)) << 4);
+    uint8_t* at1 = base + (((2 * (part & 3) + 1 - swap) ^ (row & 7)) << 4);
+#pragma unroll 2
+    for (int i = 0; i < C::N; ++i) {
+        const uint4 xi = *reinterpret_cast<const uint4*>(raw + (row + i * C::ROW_STEP) * D + part * 16);
+        const uint32_t mi = factors[row + i * C::ROW_STEP];
+        const uint32_t f = __byte_perm(mi, 0, 0x1010);
+        const uint32_t w[4] = {xi.x, xi.y, xi.z, xi.w};
         uint32_t out[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             codes4(w[j], f, out[2 * j], out[2 * j + 1]);
-        if (cs.second != 0x3F80u) {
-            const uint32_t f2 = cs.second | (cs.second << 16);
+        if (TWO) {
+            const uint32_t f2 = __byte_perm(mi, 0, 0x3232);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 out[j] = mul_bf16x2(out[j], f2);
         }
-        // 16-byte units 2 part and 2 part + 1 of the row.  With eight threads a row
-        // the upper four store theirs in the other order, so that the eight of a
-        // store fall on different banks.
         const uint4 lo = make_uint4(out[0], out[1], out[2], out[3]), hi = make_uint4(out[4], out[5], out[6], out[7]);
-        const int swap = D == 128 ? part >> 2 : 0;
-        uint8_t* at = stage + (part >> 2) * Layout<D>::KV_CHUNK + row * 128;
-        const int unit = 2 * (part & 3);
-        *reinterpret_cast<uint4*>(at + (((unit + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((unit + 1 - swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+        *reinterpret_cast<uint4*>(at0 + i * C::ROW_STEP * 128) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(at1 + i * C::ROW_STEP * 128) = swap ? lo : hi;
     }
 }
 
@@ -249,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         if (sbase & 1023u)  // the swizzled tiles need 1024-byte alignment: record it, run nothing
             report_timeout(wc, SITE_SMEM_ALIGN);
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(bar(i), i < B_EMPTY || (i >= B_P_FULL && i < B_PV_DONE) ? 128u : 1u);
+            mbar_init(bar(i), arrivals(i));
         fence_barrier_init();
     }
     if (warp == MMA_WARP) {
@@ -294,6 +313,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                     const int st = hh % L::STAGES;
                     if (!(ok = wait_all(bar(B_K_FULL + st), (hh / L::STAGES) & 1, SITE_K_FULL)))
                         break;
+                    fence_proxy_async_smem();
                     tc_fence_after();
                     const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
                     for (int t = 0; t < tiles; ++t) {
@@ -310,6 +330,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                         if (leader)
                             mma_commit(bar(B_S_FULL + 2 * t + (hh & 1)));
                     }
+                    if (leader)
+                        mma_commit(bar(B_K_EMPTY + st));
                 }
                 if (hh >= 1) {
                     const int j = hh - 1, st = j % L::STAGES, buf = j & 1;
@@ -319,6 +341,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                             break;
                         if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (j >> 1) & 1, SITE_P_FULL)))
                             break;
+                        if (t == 0)
+                            fence_proxy_async_smem();
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < STEP / 16; ++kk)
@@ -328,41 +352,98 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                             mma_commit(bar(B_PV_DONE + t));
                     }
                     if (ok && leader)
-                        mma_commit(bar(B_EMPTY + st));
+                        mma_commit(bar(B_V_EMPTY + st));
                 }
             }
             if (leader)
                 mma_commit(bar(B_O_FINAL));
             // Every MMA issued by the elected lane has completed once O_FINAL fires.
             drain_wait(bar(B_O_FINAL), 0, p.timeout_ns);
+        } else if (warp == FETCH_WARP && n > 0) {
+            // ----------------------------------------------------------- fetch
+            const int lane = threadIdx.x & 31;
+            const long long first = (bh * p.W * p.s + begin) * D;
+            // the scales of rows lane and lane + 32 of K and of V, one step ahead
+            float scale[4];
+            auto load_scales = [&](int hh) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = begin + hh * STEP + lane + 32 * (i & 1);
+                    scale[i] = 0.f;
+                    if (key < end)
+                        scale[i] = __ldg((i < 2 ? p.k_scale : p.v_scale) + scale_index(p, bh, key));
+                }
+            };
+            load_scales(0);
+            int issued = 0;
+            for (int hh = 0; hh < n; ++hh) {
+                const int rs = hh % L::RAW;
+                if (hh >= L::RAW && !__all_sync(0xFFFFFFFFu, mbar_wait(bar(B_RAW_EMPTY + rs), ((hh / L::RAW) - 1) & 1,
+                                                                       wc, SITE_RAW_EMPTY)))
+                    break;
+                uint32_t* factors = reinterpret_cast<uint32_t*>(smem + L::FACTOR_OFF) + rs * L::FACTORS;
+                bool two = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const CodeScale cs = code_scale(scale[i]);
+                    factors[32 * i + lane] = cs.first | (cs.second << 16);
+                    two |= cs.second != 0x3F80u;
+                }
+                two = __any_sync(0xFFFFFFFFu, two);
+                if (lane == 0) {
+                    factors[2 * STEP] = two ? 1u : 0u;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    const uint32_t bytes = static_cast<uint32_t>(min(STEP, end - begin - hh * STEP)) * D;
+                    const uint32_t raw = sbase + L::RAW_OFF + rs * 2 * L::RAW_TILE;
+                    const long long at = first + static_cast<long long>(hh) * L::RAW_TILE;
+                    mbar_arrive_expect_tx(bar(B_RAW_FULL + rs), 2 * bytes);
+                    bulk_load(raw, p.k8 + at, bytes, bar(B_RAW_FULL + rs));
+                    bulk_load(raw + L::RAW_TILE, p.v8 + at, bytes, bar(B_RAW_FULL + rs));
+                }
+                issued = hh + 1;
+                if (hh + 1 < n)
+                    load_scales(hh + 1);
+            }
+            // Let the copies in flight land before the block can exit: at most the last
+            // one of each stage is.
+            for (int j = max(0, issued - L::RAW); j < issued; ++j)
+                drain_wait(bar(B_RAW_FULL + j % L::RAW), (j / L::RAW) & 1, p.timeout_ns);
         }
     } else if (warp >= CONVERT_WARP) {
         // ------------------------------------------------------------- convert
         shed_registers<CONVERT_REGS>();
-        const int thread = threadIdx.x - CONVERT_WARP * 32;
-        Piece<D> k, v;
-        if (n > 0) {
-            load_piece<D>(k, p.k8, p.k_scale, p, bh, begin, end, thread);
-            load_piece<D>(v, p.v8, p.v_scale, p, bh, begin, end, thread);
-        }
+        using C = Codes<D>;
+        const int thread = threadIdx.x - CONVERT_WARP * 32, lane = thread & 31;
+        const int part = thread % C::PER_ROW, row = thread / C::PER_ROW;
         for (int hh = 0; hh < n; ++hh) {
-            const int st = hh % L::STAGES;
-            if (hh >= L::STAGES &&
-                !__all_sync(0xFFFFFFFFu, mbar_wait(bar(B_EMPTY + st), ((hh / L::STAGES) - 1) & 1, wc, SITE_EMPTY)))
+            const int st = hh % L::STAGES, rs = hh % L::RAW;
+            const uint32_t freed = ((hh / L::STAGES) - 1) & 1;
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_RAW_FULL + rs), (hh / L::RAW) & 1, wc, SITE_RAW_FULL));
+            const uint8_t* raw = smem + L::RAW_OFF + rs * 2 * L::RAW_TILE;
+            const uint32_t* factors =
+                reinterpret_cast<const uint32_t*>(smem + L::FACTOR_OFF) + rs * L::FACTORS;
+#pragma unroll 1
+            for (int kv = 0; ok && kv < 2; ++kv) {  // K, then V
+                if (hh >= L::STAGES)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar((kv ? B_V_EMPTY : B_K_EMPTY) + st), freed, wc,
+                                                           kv ? SITE_V_EMPTY : SITE_K_EMPTY));
+                if (!ok)
+                    break;
+                uint8_t* stage = smem + (kv ? L::V_OFF : L::K_OFF) + st * L::KV_TILE;
+                if (factors[2 * STEP])
+                    convert<D, true>(raw + kv * L::RAW_TILE, factors + kv * STEP, stage, row, part);
+                else
+                    convert<D, false>(raw + kv * L::RAW_TILE, factors + kv * STEP, stage, row, part);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar((kv ? B_V_FULL : B_K_FULL) + st));
+            }
+            if (!ok)
                 break;
-            const int next = begin + (hh + 1) * STEP;
-            const Piece<D> k_now = k;
-            if (hh + 1 < n)
-                load_piece<D>(k, p.k8, p.k_scale, p, bh, next, end, thread);
-            store_piece<D>(k_now, smem + L::K_OFF + st * L::KV_TILE, thread);
-            fence_proxy_async_smem();
-            mbar_arrive(bar(B_K_FULL + st));
-            const Piece<D> v_now = v;
-            if (hh + 1 < n)
-                load_piece<D>(v, p.v8, p.v_scale, p, bh, next, end, thread);
-            store_piece<D>(v_now, smem + L::V_OFF + st * L::KV_TILE, thread);
-            fence_proxy_async_smem();
-            mbar_arrive(bar(B_V_FULL + st));
+            if (lane == 0)
+                mbar_arrive(bar(B_RAW_EMPTY + rs));
         }
     } else if (warp < 4 * tiles) {
         // ------------------------------------------------------------- softmax
