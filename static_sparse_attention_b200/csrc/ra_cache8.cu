@@ -1,11 +1,16 @@
 // ra_cache8.cu -- new frames into the 8-bit key/value ring (ra_cache8.cuh), the
 // keys normed and rotated on the way.
 //
-// One thread block per (head, 64-token block of a frame, K or V): its rows are
-// read from the projection's token-major layout, normed and rotated in fp32 (K),
-// and kept in registers; the block's largest magnitude fixes the scale, the least
-// power of two that brings it to at most 448, and the codes are rounded once, to
-// nearest even, from fp32.  Bound by memory: 3 bytes a value (2 read, 1 written).
+// A thread block takes one 64-token block of a frame, K or V, and walks a group of
+// heads: its threads stay with their rows, so a row's cosines and sines and the
+// norm's weights are loaded once for all of them.  Each head's rows are read from
+// the projection's token-major layout one head ahead, normed and rotated in fp32
+// (K), and kept in registers; the block's largest magnitude fixes the scale, the
+// least power of two that brings it to at most 448, and the codes are rounded once,
+// to nearest even, from fp32.  Bound by memory: 3 bytes a value (2 read, 1 written).
+// With a thread block for each head the position look-up was a third of the
+// instructions, and the issue slots the bound: 247 us for 12 frames of 3555 tokens,
+// 24 heads of 128.
 //
 // The scale's power of two costs no precision against amax / 448: e4m3 is a
 // floating format, so only the numbers near its subnormals (2^-15 of the largest
@@ -26,6 +31,8 @@ namespace {
 
 constexpr int PASSES = 4;         // row groups of a block held in registers
 constexpr int ROWS_PER_PASS = 16; // so that PASSES * ROWS_PER_PASS rows make a block
+constexpr int HEADS_MAX = 8;
+constexpr int WANT_BLOCKS = 148 * 4;
 static_assert(PASSES * ROWS_PER_PASS == CACHE8_BLOCK, "a block of tokens is held whole");
 
 struct AppendParams {
@@ -36,103 +43,130 @@ struct AppendParams {
     const void* weight;         // norm of K, or null
     int weight_fp32;
     int H, s, W, blocks, slot0;
+    int groups, heads;          // groups of heads, heads of a group
     RopeArgs rope;
     float eps;
 };
 
-template <int D>
-__global__ void __launch_bounds__(ROWS_PER_PASS * D / 8) cache8_append_kernel(const AppendParams p)
+// The larger magnitude; NaN if one is.
+__device__ __forceinline__ float max_abs(float m, float a, float b)
 {
-    constexpr int LPR = D / 8;
-    const int which = blockIdx.y, b = blockIdx.z;
-    const int h = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.H));
-    const int fb = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.H));
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+    return d;
+}
+
+template <int D>
+struct Shared {
+    uint32_t tops[2][ROWS_PER_PASS * D / 256];  // each warp's largest magnitude
+    // Cosines and sines, [row][lane of the row]: each thread's own, here rather than
+    // in 32 of its registers.
+    float4 turns[CACHE8_BLOCK][D / 8][2];
+};
+
+template <int D, bool KEYS>
+__device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& shared)
+{
+    constexpr int LPR = D / 8, WHICH = KEYS ? 0 : 1;
+    const int b = blockIdx.z;
+    const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.groups));
+    const int fb = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
     const int frame = fb / p.blocks, blk = fb - frame * p.blocks;
     const int rows = min(CACHE8_BLOCK, p.s - blk * CACHE8_BLOCK);
     const int sub = threadIdx.x % LPR, row0 = threadIdx.x / LPR, step = blockDim.x / LPR;
     const int token0 = frame * p.s + blk * CACHE8_BLOCK;  // among the call's tokens
-    const __nv_bfloat16* x = p.x[which] + b * p.sb[which] + h * p.sh[which] + sub * 8;
-    uint4 v[PASSES];
+    const int h0 = group * p.heads, h1 = min(h0 + p.heads, p.H);
+    const __nv_bfloat16* x = p.x[WHICH] + b * p.sb[WHICH] + (token0 + row0) * p.sn[WHICH] + sub * 8;
+    auto load = [&](uint4 (&v)[PASSES], int h) {
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = row0 + i * step;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-            v[i] = __ldcs(reinterpret_cast<const uint4*>(x + static_cast<long long>(token0 + r) * p.sn[which]));
-    }
-    float f[PASSES][8];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-        unpack_bf16x8(v[i], f[i]);
-    if (which == 0) {
-        if (p.weight) {
-            float w[8];
-            load_weight(p.weight, p.weight_fp32, sub, w);
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i)
-                rms_norm<D>(f[i], w, p.eps);
+        for (int i = 0; i < PASSES; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (row0 + i * step < rows)
+                v[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * p.sh[WHICH] + i * step * p.sn[WHICH]));
         }
+    };
+    uint4 next[PASSES];
+    load(next, h0);
+    float w[8];
+    if (KEYS) {
+        if (p.weight)
+            load_weight(p.weight, p.weight_fp32, sub, w);
         if (p.rope.t) {
-#pragma unroll
-            for (int i = 0; i < PASSES; ++i) {
-                if (row0 + i * step < rows) {
-                    float2 cs[4];
-                    load_rope(p.rope, token0 + row0 + i * step, sub, cs);
-                    rotate(cs, f[i]);
-                }
+            for (int r = row0; r < rows; r += step) {
+                float2 cs[4];
+                load_rope(p.rope, token0 + r, sub, cs);
+                shared.turns[r][sub][0] = make_float4(cs[0].x, cs[0].y, cs[1].x, cs[1].y);
+                shared.turns[r][sub][1] = make_float4(cs[2].x, cs[2].y, cs[3].x, cs[3].y);
             }
         }
     }
-    // the largest magnitude as bits: above every finite number for infinities and NaN
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            top = max(top, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    __shared__ uint32_t tops[ROWS_PER_PASS * LPR / 32];
-    if (blockDim.x > 32) {
-        if (threadIdx.x % 32 == 0)
-            tops[threadIdx.x / 32] = top;
-        __syncthreads();
-        for (unsigned k = 0; k < blockDim.x / 32; ++k)
-            top = max(top, tops[k]);
-    }
-    // scale = 2^k: largest = 1.m * 2^e, k = e - 8, one more above 448 = 1.75 * 2^8
-    float scale = 1.f, inverse = 1.f;
-    if (top >= 0x7F800000u) {
-        scale = __uint_as_float(0x7FFFFFFFu);
-        inverse = 0.f;  // codes of such a block are zero or, from infinities and NaN, the format's largest
-    } else if (top > 0) {
-        int k = static_cast<int>(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        k = max(k, -126);
-        scale = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-        inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-    }
     const int slot = (p.slot0 + frame) % p.W;
-    const long long slot_of_head = (static_cast<long long>(b) * p.H + h) * p.W + slot;
-    uint8_t* code = p.code[which] + (slot_of_head * p.s + blk * CACHE8_BLOCK) * D + sub * 8;
+    for (int h = h0; h < h1; ++h) {
+        float f[PASSES][8];
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-        const int r = row0 + i * step;
-        if (r >= rows)
-            continue;
-        uint32_t word[2];
+        for (int i = 0; i < PASSES; ++i)
+            unpack_bf16x8(next[i], f[i]);
+        if (h + 1 < h1)
+            load(next, h + 1);
+        float top = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t half[2];
+        for (int i = 0; i < PASSES; ++i) {
+            if (KEYS) {
+                if (p.weight)
+                    rms_norm<D>(f[i], w, p.eps);
+                if (p.rope.t && row0 + i * step < rows) {
+                    const float4 a = shared.turns[row0 + i * step][sub][0], c = shared.turns[row0 + i * step][sub][1];
+                    const float2 cs[4] = {{a.x, a.y}, {a.z, a.w}, {c.x, c.y}, {c.z, c.w}};
+                    rotate(cs, f[i]);
+                }
+            }
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                half[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[i][4 * j + 2 * e] * inverse,
-                                                               f[i][4 * j + 2 * e + 1] * inverse),
-                                                   __NV_SATFINITE, __NV_E4M3);
-            word[j] = top >= 0x7F800000u ? 0u : half[0] | (half[1] << 16);
+            for (int j = 0; j < 8; j += 2)
+                top = max_abs(top, f[i][j], f[i][j + 1]);
         }
-        *reinterpret_cast<uint2*>(code + static_cast<size_t>(r) * D) = make_uint2(word[0], word[1]);
+        // as bits, magnitudes compare like numbers, infinities and NaN above the finite ones
+        uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+        if (blockDim.x > 32) {
+            uint32_t(&mine)[ROWS_PER_PASS * D / 256] = shared.tops[h & 1];  // two sets: the last head's may still be read
+            if (threadIdx.x % 32 == 0)
+                mine[threadIdx.x / 32] = bits;
+            __syncthreads();
+            for (unsigned k = 0; k < blockDim.x / 32; ++k)
+                bits = max(bits, mine[k]);
+        }
+        // scale = 2^k: largest = 1.m * 2^e, k = e - 8, one more above 448 = 1.75 * 2^8
+        const bool finite = bits < 0x7F800000u;
+        int k = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        k = bits == 0 ? 0 : max(k, -126);
+        const float scale = __uint_as_float(finite ? static_cast<uint32_t>(k + 127) << 23 : 0x7FFFFFFFu);
+        const float inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+        const long long slot_of_head = (static_cast<long long>(b) * p.H + h) * p.W + slot;
+        uint8_t* code = p.code[WHICH] + (slot_of_head * p.s + blk * CACHE8_BLOCK + row0) * D + sub * 8;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            uint32_t half[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                half[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[i][2 * e] * inverse, f[i][2 * e + 1] * inverse),
+                                                   __NV_SATFINITE, __NV_E4M3);
+            const uint2 word = finite ? make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16))
+                                      : make_uint2(0, 0);
+            if (row0 + i * step < rows)
+                *reinterpret_cast<uint2*>(code + static_cast<size_t>(i) * step * D) = word;
+        }
+        if (threadIdx.x == 0)
+            p.scale[WHICH][slot_of_head * p.blocks + blk] = scale;
     }
-    if (threadIdx.x == 0)
-        p.scale[which][slot_of_head * p.blocks + blk] = scale;
+}
+
+template <int D>
+__global__ void __launch_bounds__(ROWS_PER_PASS * D / 8, 3 * 128 / D) cache8_append_kernel(const AppendParams p)
+{
+    __shared__ Shared<D> shared;
+    if (blockIdx.y == 0)
+        append_block<D, true>(p, shared);
+    else
+        append_block<D, false>(p, shared);
 }
 
 }  // namespace
@@ -224,7 +258,13 @@ extern "C" ra_status ra_cache8_append(const ra_head_rows* k, const ra_head_rows*
             if (overlap(out[i], out[j]))
                 return fail(RA_ERR_INVALID_ARG, "the rings and scales may not alias one another");
     }
-    const long long blocks = static_cast<long long>(frames) * p.blocks * H;
+    // heads of a thread block: up to HEADS_MAX, fewer while that leaves SMs without work
+    const long long units = static_cast<long long>(frames) * p.blocks;
+    p.heads = HEADS_MAX;
+    while (p.heads > 1 && units * B * 2 * ((H + p.heads - 1) / p.heads) < WANT_BLOCKS)
+        p.heads /= 2;
+    p.groups = (H + p.heads - 1) / p.heads;
+    const long long blocks = units * p.groups;
     if (blocks > (1LL << 31) - 1)
         return fail(RA_ERR_UNSUPPORTED, "too many blocks in one call (%lld)", blocks);
     const dim3 grid(static_cast<unsigned>(blocks), 2, B);

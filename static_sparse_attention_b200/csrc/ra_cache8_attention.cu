@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
 // blocks for every SM.  Many: the number of ranges with the least estimated time,
 // counted in steps of 64 keys of the 256-query kernel (one block an SM).
 constexpr int MIN_CHUNK = 256;
+constexpr int WHOLE = 512;  // as many keys as one block takes in less time than the join's launch
 constexpr int SMS = 148;
 constexpr int WANT_BLOCKS = SMS * 8;
 constexpr int TILES_MIN_QUERIES = 33;  // more queries than this go to the many-query kernel
@@ -360,7 +361,7 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
         }
     } else {
         splits = (WANT_BLOCKS + tiles - 1) / tiles;
-        const long long most = (static_cast<long long>(nk) + MIN_CHUNK - 1) / MIN_CHUNK;
+        const long long most = nk <= WHOLE ? 1 : (static_cast<long long>(nk) + MIN_CHUNK - 1) / MIN_CHUNK;
         splits = splits < most ? splits : most;
         splits = splits < 1 ? 1 : splits;
     }

@@ -30,7 +30,12 @@ namespace {
 constexpr int THREADS = 256;
 constexpr int HEADS_MAX = 8;        // heads that a lane walks for one token
 constexpr int HEADS_IN_FLIGHT = 4;  // rows loaded before the first is used
-constexpr int BWD_BLOCKS = 592;     // partial sums of a weight's gradient: 4 blocks on each of 148 SMs
+// The backward keeps 24 warps an SM: at 16 (122 registers a thread, nothing asked of
+// the compiler) 63960 tokens of 40 heads of 128 take 778 us, at 24 (85 registers)
+// 690, at 32 (64 registers, spills) 830.
+constexpr int BWD_BLOCKS_PER_SM = 3;
+constexpr int BWD_BLOCKS = 148 * BWD_BLOCKS_PER_SM;  // and as many partial sums of a weight's gradient
+constexpr int FWD_WANT_BLOCKS = 148 * 4;
 
 // One of the two tensors (q or k) of a call.
 struct Rows {
@@ -101,7 +106,7 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
 }
 
 template <int D>
-__global__ void __launch_bounds__(THREADS) qk_norm_rope_bwd_kernel(const Params p)
+__global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_kernel(const Params p)
 {
     constexpr int LPR = D / 8, TOKENS = THREADS / LPR;
     const Rows& t = p.t[blockIdx.y];
@@ -357,7 +362,7 @@ ra_status check_sizes(int B, int n, int d, float eps)
 int heads_per_chunk(long long tiles, int B, int H)
 {
     int heads = HEADS_MAX;
-    while (heads > 1 && tiles * B * ((H + heads - 1) / heads) < BWD_BLOCKS)
+    while (heads > 1 && tiles * B * ((H + heads - 1) / heads) < FWD_WANT_BLOCKS)
         heads /= 2;
     return heads;
 }
