@@ -64,29 +64,35 @@ struct Shared {
     float4 turns[CACHE8_BLOCK][D / 8][2];
 };
 
-template <int D, bool KEYS>
+// FULL: a block of 64 tokens and all threads.
+template <int D, bool KEYS, bool FULL>
 __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& shared)
 {
-    constexpr int LPR = D / 8, WHICH = KEYS ? 0 : 1;
+    constexpr int LPR = D / 8, WHICH = KEYS ? 0 : 1, WARPS = ROWS_PER_PASS * LPR / 32;
     const int b = blockIdx.z;
     const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.groups));
     const int fb = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups));
     const int frame = fb / p.blocks, blk = fb - frame * p.blocks;
-    const int rows = min(CACHE8_BLOCK, p.s - blk * CACHE8_BLOCK);
-    const int sub = threadIdx.x % LPR, row0 = threadIdx.x / LPR, step = blockDim.x / LPR;
+    const int rows = FULL ? CACHE8_BLOCK : min(CACHE8_BLOCK, p.s - blk * CACHE8_BLOCK);
+    const int step = FULL ? ROWS_PER_PASS : blockDim.x / LPR;
+    const int sub = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
     const int token0 = frame * p.s + blk * CACHE8_BLOCK;  // among the call's tokens
     const int h0 = group * p.heads, h1 = min(h0 + p.heads, p.H);
-    const __nv_bfloat16* x = p.x[WHICH] + b * p.sb[WHICH] + (token0 + row0) * p.sn[WHICH] + sub * 8;
-    auto load = [&](uint4 (&v)[PASSES], int h) {
+    const __nv_bfloat16* x =
+        p.x[WHICH] + b * p.sb[WHICH] + h0 * p.sh[WHICH] + (token0 + row0) * p.sn[WHICH] + sub * 8;
+    const long long row_step = step * p.sn[WHICH];
+    auto in = [&](int i) { return FULL || row0 + i * step < rows; };
+    auto load = [&](uint4 (&v)[PASSES]) {  // the head that x stands at
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-            if (row0 + i * step < rows)
-                v[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * p.sh[WHICH] + i * step * p.sn[WHICH]));
+            if (in(i))
+                v[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * row_step));
         }
+        x += p.sh[WHICH];
     };
     uint4 next[PASSES];
-    load(next, h0);
+    load(next);
     float w[8];
     if (KEYS) {
         if (p.weight)
@@ -100,62 +106,98 @@ __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& s
             }
         }
     }
+    long long head = static_cast<long long>(b) * p.H + h0;
     const int slot = (p.slot0 + frame) % p.W;
+    const long long first = (head * p.W + slot) * p.s + blk * CACHE8_BLOCK + row0, next_head = static_cast<long long>(p.W) * p.s;
+    uint8_t* code = p.code[WHICH] + first * D + sub * 8;
     for (int h = h0; h < h1; ++h) {
-        float f[PASSES][8];
+        // f: the row before the norm's factor r, which joins the scale's below
+        float f[PASSES][8], r[PASSES];
 #pragma unroll
         for (int i = 0; i < PASSES; ++i)
             unpack_bf16x8(next[i], f[i]);
         if (h + 1 < h1)
-            load(next, h + 1);
-        float top = 0.f;
+            load(next);
+        if (KEYS && p.weight) {
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            if (KEYS) {
-                if (p.weight)
-                    rms_norm<D>(f[i], w, p.eps);
-                if (p.rope.t && row0 + i * step < rows) {
+            for (int i = 0; i < PASSES; ++i) {
+                float ss = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    ss = fmaf(f[i][j], f[i][j], ss);
+                r[i] = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + p.eps);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[i][j] *= w[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i)
+                r[i] = 1.f;
+        }
+        if (KEYS && p.rope.t) {
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                if (in(i)) {
                     const float4 a = shared.turns[row0 + i * step][sub][0], c = shared.turns[row0 + i * step][sub][1];
                     const float2 cs[4] = {{a.x, a.y}, {a.z, a.w}, {c.x, c.y}, {c.z, c.w}};
                     rotate(cs, f[i]);
                 }
             }
+        }
+        float top = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; j += 2)
-                top = max_abs(top, f[i][j], f[i][j + 1]);
+        for (int i = 0; i < PASSES; ++i) {
+            float m = max_abs(0.f, f[i][0], f[i][1]);
+#pragma unroll
+            for (int j = 2; j < 8; j += 2)
+                m = max_abs(m, f[i][j], f[i][j + 1]);
+            top = max_abs(top, m * r[i], 0.f);
         }
         // as bits, magnitudes compare like numbers, infinities and NaN above the finite ones
         uint32_t bits = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
-        if (blockDim.x > 32) {
-            uint32_t(&mine)[ROWS_PER_PASS * D / 256] = shared.tops[h & 1];  // two sets: the last head's may still be read
-            if (threadIdx.x % 32 == 0)
-                mine[threadIdx.x / 32] = bits;
+        if (FULL || blockDim.x > 32) {
+            uint32_t(&tops)[WARPS] = shared.tops[h & 1];  // two sets: the last head's may still be read
+            const int lane = threadIdx.x & 31;
+            if (lane == 0)
+                tops[threadIdx.x / 32] = bits;
             __syncthreads();
-            for (unsigned k = 0; k < blockDim.x / 32; ++k)
-                bits = max(bits, mine[k]);
+            bits = __reduce_max_sync(0xFFFFFFFFu, lane < (FULL ? WARPS : static_cast<int>(blockDim.x) / 32) ? tops[lane] : 0u);
         }
         // scale = 2^k: largest = 1.m * 2^e, k = e - 8, one more above 448 = 1.75 * 2^8
         const bool finite = bits < 0x7F800000u;
         int k = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-        k = bits == 0 ? 0 : max(k, -126);
-        const float scale = __uint_as_float(finite ? static_cast<uint32_t>(k + 127) << 23 : 0x7FFFFFFFu);
-        const float inverse = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-        const long long slot_of_head = (static_cast<long long>(b) * p.H + h) * p.W + slot;
-        uint8_t* code = p.code[WHICH] + (slot_of_head * p.s + blk * CACHE8_BLOCK + row0) * D + sub * 8;
+        k = bits == 0 || !finite ? 0 : max(k, -126);
+        if (threadIdx.x == 0)
+            p.scale[WHICH][(head * p.W + slot) * p.blocks + blk] =
+                __uint_as_float(finite ? static_cast<uint32_t>(k + 127) << 23 : 0x7FFFFFFFu);
+        // 1 / scale, in two factors where r * (1 / scale) would overflow
+        const int k1 = max(k, -100);
+        const float inverse = __uint_as_float(static_cast<uint32_t>(127 - k1) << 23);
+        if (k1 != k) {
+            const float rest = __uint_as_float(static_cast<uint32_t>(127 + k1 - k) << 23);
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    f[i][j] *= rest;
+        }
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
+            const float by = r[i] * inverse;
             uint32_t half[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                half[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[i][2 * e] * inverse, f[i][2 * e + 1] * inverse),
-                                                   __NV_SATFINITE, __NV_E4M3);
-            const uint2 word = finite ? make_uint2(half[0] | (half[1] << 16), half[2] | (half[3] << 16))
-                                      : make_uint2(0, 0);
-            if (row0 + i * step < rows)
+                half[e] = __nv_cvt_float2_to_fp8x2(make_float2(f[i][2 * e] * by, f[i][2 * e + 1] * by), __NV_SATFINITE,
+                                                   __NV_E4M3);
+            uint2 word = make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
+            if (!finite)
+                word = make_uint2(0, 0);
+            if (in(i))
                 *reinterpret_cast<uint2*>(code + static_cast<size_t>(i) * step * D) = word;
         }
-        if (threadIdx.x == 0)
-            p.scale[WHICH][slot_of_head * p.blocks + blk] = scale;
+        ++head;
+        code += next_head * D;
     }
 }
 
@@ -163,10 +205,19 @@ template <int D>
 __global__ void __launch_bounds__(ROWS_PER_PASS * D / 8, 3 * 128 / D) cache8_append_kernel(const AppendParams p)
 {
     __shared__ Shared<D> shared;
-    if (blockIdx.y == 0)
-        append_block<D, true>(p, shared);
-    else
-        append_block<D, false>(p, shared);
+    const int blk = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.groups)) % p.blocks;
+    const bool full = p.s - blk * CACHE8_BLOCK >= CACHE8_BLOCK;
+    if (blockIdx.y == 0) {
+        if (full)
+            append_block<D, true, true>(p, shared);
+        else
+            append_block<D, true, false>(p, shared);
+    } else {
+        if (full)
+            append_block<D, false, true>(p, shared);
+        else
+            append_block<D, false, false>(p, shared);
+    }
 }
 
 }  // namespace
