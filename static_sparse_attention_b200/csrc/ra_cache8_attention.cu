@@ -2,15 +2,22 @@
 // key/value ring (ra_cache8.cuh):
 //     O = softmax(scale * Q K^T) V over the first count keys of each head.
 //
-// Few-query kernel: one block per (head, 16 queries, range of keys), four warps
-// that take groups of 16 keys in turn.  Codes go from memory to registers and are
-// turned to bf16 there; both products are 16 x 8 x 16 warp products with fp32
-// sums.  The order of channels and keys inside a product is free, so it is chosen
-// by what a lane loads: 16 contiguous bytes of a key's row for S, and of a
-// value's row for P V.  Ranges of keys leave partial (maximum, sum, O) to a
-// second kernel that joins them.  Bound by memory for few queries (one byte a
-// value of K and V).
+// Few-query kernel: one block per (head, 8 or 16 queries, range of keys), four
+// warps that take groups of 16 keys in turn, the next group on its way while one is
+// computed.  Both products are 16 x 8 x 16 warp products with fp32 sums that keep the
+// queries as columns: S^T = K Q^T and O^T += V^T P^T, so that eight queries (or one)
+// take half the registers that they would as rows.  The order of channels and keys
+// inside a product is free and chosen by what a lane loads: 16 contiguous bytes of a
+// key's row, and of a value's row.
+//   S^T: the codes go to fp16 as they are (one instruction for two), Q is brought to
+//        fp16 by a power of two for each query, and the key's scale multiplies the
+//        score.
+//   P V: the values go to bf16 code * scale (ra_cache8.cuh) and P to bf16, whose
+//        range no mixture of scales leaves.
+// Ranges of keys leave partial (maximum, sum, O) to a second kernel that joins them.
+// Bound by memory for few queries (one byte a value of K and V).
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -22,9 +29,10 @@
 namespace ra {
 namespace {
 
-constexpr int ROWS = 16;   // queries of a block
+constexpr int COLS = 8;    // queries of a product
 constexpr int WARPS = 4;
 constexpr int GROUP = 16;  // keys that a warp takes at a time
+constexpr int PREFETCH = 4;  // rounds of groups that L2 is asked for ahead
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -38,14 +46,41 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// D += A B: A 16 x 16 (row), B 16 x 8 (column), bf16, fp32 sums.
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+// D += A B: A 16 x 16 (row), B 16 x 8 (column), fp32 sums.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
 {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit numbers spread over the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Codes 0, 1 and codes 2, 3 of a word as fp16 numbers.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // Codes and scales of one group of keys, as a lane (r = lane / 4, c = lane % 4) holds them.
@@ -58,123 +93,157 @@ struct Group {
     float scale;                        // lanes 0-15: of key lane, 16-31: of value lane - 16 (0 behind the range)
 };
 
+// Where a lane reads: its places in the rows of the group that starts at key 0 of
+// the head.
+struct Places {
+    const uint8_t* k;     // row r
+    const uint8_t* v;     // row 2 c
+    const uint8_t* ahead; // of K (lanes 0-15) or V: row lane % 16, for the prefetch
+    const float* scale;   // of K or V
+};
+
 template <int D>
-__device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, long long bh, int key0, int end)
+__device__ __forceinline__ Places places_of(const AttnParams& p, long long bh)
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const long long head = bh * p.W * p.s;
+    const long long head = bh * p.W * p.s * D;
+    return Places{p.k8 + head + r * D + 16 * c, p.v8 + head + 2 * c * D + r * (D / 8),
+                  (lane < 16 ? p.k8 : p.v8) + head + (lane & 15) * D, lane < 16 ? p.k_scale : p.v_scale};
+}
+
+template <int D, bool WHOLE_GROUP>
+__device__ __forceinline__ void load_codes(Group<D>& g, const Places& at, int key0, int end)
+{
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const uint8_t *k = at.k + static_cast<long long>(key0) * D, *v = at.v + static_cast<long long>(key0) * D;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int key = key0 + 8 * t + r;
 #pragma unroll
         for (int i = 0; i < Group<D>::KP; ++i) {
-            g.k[t][i] = make_uint4(0, 0, 0, 0);
-            if (key < end)
-                g.k[t][i] = __ldcs(reinterpret_cast<const uint4*>(p.k8 + (head + key) * D + 64 * i + 16 * c));
+            if (!WHOLE_GROUP)
+                g.k[t][i] = make_uint4(0, 0, 0, 0);
+            if (WHOLE_GROUP || key0 + 8 * t + r < end)
+                g.k[t][i] = __ldcs(reinterpret_cast<const uint4*>(k + 8 * t * D + 64 * i));
         }
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-        const int key = key0 + 2 * c + (t & 1) + 8 * (t >> 1);
+        const int row = (t & 1) + 8 * (t >> 1);  // behind 2 c
+        if (!WHOLE_GROUP) {
 #pragma unroll
-        for (int i = 0; i < Group<D>::VW; ++i)
-            g.v[t][i] = 0;
-        if (key < end) {
-            const uint8_t* at = p.v8 + (head + key) * D + r * (D / 8);
+            for (int i = 0; i < Group<D>::VW; ++i)
+                g.v[t][i] = 0;
+        }
+        if (WHOLE_GROUP || key0 + 2 * c + row < end) {
             if (D == 128) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(at));
+                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(v + row * D));
                 g.v[t][0] = w.x, g.v[t][1] = w.y, g.v[t][Group<D>::VW - 2] = w.z, g.v[t][Group<D>::VW - 1] = w.w;
             } else {
-                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(at));
+                const uint2 w = __ldcs(reinterpret_cast<const uint2*>(v + row * D));
                 g.v[t][0] = w.x, g.v[t][1] = w.y;
             }
         }
     }
-    const int key = key0 + (lane & 15);
-    g.scale = 0.f;
-    if (key < end) {
-        const long long at = scale_index(p, bh, key);
-        g.scale = lane < 16 ? p.k_scale[at] : p.v_scale[at];
-    }
 }
 
-// The running state of 16 queries in one warp: rows r and r + 8 of the tile.
+// The group that starts at key0: its codes (zeros behind `end`) and scales; and ask
+// L2 for the rows of one PREFETCH rounds later, one of K or V a lane.
 template <int D>
+__device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, const Places& at, long long bh, int key0,
+                                           int end)
+{
+    if (key0 + GROUP <= end)
+        load_codes<D, true>(g, at, key0, end);
+    else
+        load_codes<D, false>(g, at, key0, end);
+    const int key = key0 + static_cast<int>(threadIdx.x & 15);
+    g.scale = key < end ? at.scale[scale_index(p, bh, key)] : 0.f;
+    const int later = key0 + PREFETCH * WARPS * GROUP;
+    if (later + GROUP <= end)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at.ahead + static_cast<long long>(later) * D));
+}
+
+// The running state of 8 NT queries in one warp: a lane holds queries 8 t + 2 c and
+// 8 t + 2 c + 1.
+template <int D, int NT>
 struct State {
-    uint32_t q[D / 16][4];  // A operands of S
-    float o[D / 8][4];
-    float m[2], l[2];       // l: this lane's keys only
+    uint32_t q[D / 16][NT][2];  // B operands of S^T
+    float unit[NT][2];          // scale * log2(e) * the query's power of two
+    float o[D / 16][NT][4];     // O^T: channels (D / 8) r + 2 i and the next
+    float m[NT][2], l[NT][2];   // l: this lane's keys only
 };
 
 // TWO: some scale of the group needs its second factor.
-template <int D, bool TWO>
-__device__ __forceinline__ void group_step(State<D>& st, const Group<D>& g, int key0, int end, float scale_log2)
+template <int D, int NT, bool TWO>
+__device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, int key0, int end)
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const CodeScale mine = code_scale(g.scale);
-    const uint32_t both = mine.first | (mine.second << 16);
-    float s[2][4];
+    float s[NT][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const uint32_t f = __shfl_sync(0xFFFFFFFFu, both, 8 * t + r);
-        const uint32_t f1 = __byte_perm(f, 0, 0x1010), f2 = __byte_perm(f, 0, 0x3232);
+    for (int t = 0; t < NT; ++t)
         s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < Group<D>::KP; ++i) {
-            const uint32_t w[4] = {g.k[t][i].x, g.k[t][i].y, g.k[t][i].z, g.k[t][i].w};
+    for (int i = 0; i < Group<D>::KP; ++i) {
+        const uint32_t w0[4] = {g.k[0][i].x, g.k[0][i].y, g.k[0][i].z, g.k[0][i].w};
+        const uint32_t w1[4] = {g.k[1][i].x, g.k[1][i].y, g.k[1][i].z, g.k[1][i].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t b0 = mul_bf16x2(e4m3x2_small(w[j] << 8), f1);
-                uint32_t b1 = mul_bf16x2(e4m3x2_small(w[j]), f1);
-                if (TWO) {
-                    b0 = mul_bf16x2(b0, f2);
-                    b1 = mul_bf16x2(b1, f2);
-                }
-                mma16816(s[t], st.q[4 * i + j], b0, b1);
-            }
+        for (int j = 0; j < 4; ++j) {
+            uint32_t a[4];
+            codes_to_f16(w0[j], a[0], a[2]);
+            codes_to_f16(w1[j], a[1], a[3]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                mma_f16(s[t], a, st.q[4 * i + j][t][0], st.q[4 * i + j][t][1]);
         }
     }
-    // online softmax in base 2, keys behind the range masked
-    float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[t][e] = key0 + 8 * t + 2 * c + (e & 1) < end ? __fmul_rn(s[t][e], scale_log2) : -INFINITY;
-            top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
-        }
+    // online softmax in base 2: rows r and r + 8 are keys, those behind the range masked
+    const float k0 = __shfl_sync(0xFFFFFFFFu, g.scale, r), k1 = __shfl_sync(0xFFFFFFFFu, g.scale, 8 + r);
+    const bool in0 = key0 + r < end, in1 = key0 + 8 + r < end;
     bool grew = false;
-    float use[2], alpha[2];
+    float alpha[NT][2], use[NT][2];
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        top[y] = fmaxf(top[y], __shfl_xor_sync(0xFFFFFFFFu, top[y], 1));
-        top[y] = fmaxf(top[y], __shfl_xor_sync(0xFFFFFFFFu, top[y], 2));
-        const float m = fmaxf(st.m[y], top[y]);
-        alpha[y] = m == -INFINITY ? 1.f : exp2_fast(st.m[y] - m);
-        grew |= m > st.m[y];
-        st.m[y] = m;
-        use[y] = m == -INFINITY ? 0.f : m;  // no finite score yet: 2^(-inf) = 0, and a NaN stays one
-    }
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            s[t][y] = in0 ? __fmul_rn(s[t][y] * st.unit[t][y], k0) : -INFINITY;
+            s[t][2 + y] = in1 ? __fmul_rn(s[t][2 + y] * st.unit[t][y], k1) : -INFINITY;
+            float top = fmaxf(s[t][y], s[t][2 + y]);
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            const float m = fmaxf(st.m[t][y], top);
+            alpha[t][y] = m == -INFINITY ? 1.f : exp2_fast(st.m[t][y] - m);
+            grew |= m > st.m[t][y];
+            st.m[t][y] = m;
+            use[t][y] = m == -INFINITY ? 0.f : m;  // no finite score yet: 2^(-inf) = 0, and a NaN stays one
+        }
     if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            st.o[j][0] *= alpha[0];
-            st.o[j][1] *= alpha[0];
-            st.o[j][2] *= alpha[1];
-            st.o[j][3] *= alpha[1];
-        }
-        st.l[0] *= alpha[0];
-        st.l[1] *= alpha[1];
-    }
+        for (int t = 0; t < NT; ++t) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+            for (int i = 0; i < D / 16; ++i) {
+                st.o[i][t][0] *= alpha[t][0];
+                st.o[i][t][1] *= alpha[t][1];
+                st.o[i][t][2] *= alpha[t][0];
+                st.o[i][t][3] *= alpha[t][1];
+            }
+            st.l[t][0] *= alpha[t][0];
+            st.l[t][1] *= alpha[t][1];
+        }
+    }
+    uint32_t b0[NT], b1[NT];  // P^T: keys 2 c, 2 c + 1 (b0) and 8 more (b1) of query r
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[t][e] = exp2_fast(s[t][e] - use[e >> 1]);
-            st.l[e >> 1] += s[t][e];
+            s[t][e] = exp2_fast(s[t][e] - use[t][e & 1]);
+            st.l[t][e & 1] += s[t][e];
         }
-    const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
-                           pack2(s[1][2], s[1][3])};
+        b0[t] = transpose8x8(pack2(s[t][0], s[t][1]));
+        b1[t] = transpose8x8(pack2(s[t][2], s[t][3]));
+    }
+    const CodeScale mine = code_scale(g.scale);
+    const uint32_t both = mine.first | (mine.second << 16);
     uint32_t f1[2], f2[2];  // of the value pairs 2 c, 2 c + 1 and 8 + 2 c, 9 + 2 c
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -184,22 +253,30 @@ __device__ __forceinline__ void group_step(State<D>& st, const Group<D>& g, int 
         f2[t] = __byte_perm(x, y, 0x7632);
     }
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-        // byte j of each pair of keys, to bytes 1 and 3 (the others are masked out)
-        const uint32_t pick = static_cast<uint32_t>(((4 + j % 4) << 12) | ((j % 4) << 4));
-        uint32_t b0 = mul_bf16x2(e4m3x2_small(__byte_perm(g.v[0][j / 4], g.v[1][j / 4], pick)), f1[0]);
-        uint32_t b1 = mul_bf16x2(e4m3x2_small(__byte_perm(g.v[2][j / 4], g.v[3][j / 4], pick)), f1[1]);
-        if (TWO) {
-            b0 = mul_bf16x2(b0, f2[0]);
-            b1 = mul_bf16x2(b1, f2[1]);
+    for (int i = 0; i < D / 16; ++i) {
+        uint32_t a[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // byte 2 i + e of each pair of keys, to bytes 1 and 3 (the others are masked out)
+            const int word = (2 * i + e) / 4, byte = (2 * i + e) % 4;
+            const uint32_t pick = static_cast<uint32_t>(((4 + byte) << 12) | (byte << 4));
+            a[e] = mul_bf16x2(e4m3x2_small(__byte_perm(g.v[0][word], g.v[1][word], pick)), f1[0]);
+            a[2 + e] = mul_bf16x2(e4m3x2_small(__byte_perm(g.v[2][word], g.v[3][word], pick)), f1[1]);
+            if (TWO) {
+                a[e] = mul_bf16x2(a[e], f2[0]);
+                a[2 + e] = mul_bf16x2(a[2 + e], f2[1]);
+            }
         }
-        mma16816(st.o[j], a, b0, b1);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+            mma_bf16(st.o[i][t], a, b0[t], b1[t]);
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(WARPS * 32) cache8_rows_kernel(const AttnParams p)
+template <int D, int NT>
+__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kernel(const AttnParams p)
 {
+    constexpr int ROWS = COLS * NT;
     __shared__ float sm_o[WARPS][ROWS][D + 4];
     __shared__ float sm_m[WARPS][ROWS], sm_l[WARPS][ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -213,52 +290,85 @@ __global__ void __launch_bounds__(WARPS * 32) cache8_rows_kernel(const AttnParam
     const int end = min(begin + p.chunk, count);
     const int q0 = q_tile * ROWS;
 
-    State<D> st;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            uint2 w = make_uint2(0, 0);
-            const int q = q0 + r + 8 * y;
-            if (q < p.nq)
-                w = *reinterpret_cast<const uint2*>(p.Q + (bh * p.nq + q) * D + 64 * (i / 4) + 16 * c + 4 * (i % 4));
-            st.q[i][y] = __byte_perm(w.x, w.y, 0x5410);      // channels 0, 2 of the four
-            st.q[i][2 + y] = __byte_perm(w.x, w.y, 0x7632);  // channels 1, 3
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < D / 8; ++j)
-        st.o[j][0] = st.o[j][1] = st.o[j][2] = st.o[j][3] = 0.f;
-    st.m[0] = st.m[1] = -INFINITY;
-    st.l[0] = st.l[1] = 0.f;
-
-    Group<D> g;
+    // two groups in registers, taken in turn: one on its way while the other is computed
+    Group<D> even, odd;
+    const Places at = places_of<D>(p, bh);
     int key = begin + warp * GROUP;
     if (key < end)
-        load_group(g, p, bh, key, end);
-    for (; key < end; key += WARPS * GROUP) {
-        const Group<D> now = g;
+        load_group(even, p, at, bh, key, end);
+
+    State<D, NT> st;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        // query 8 t + r: a quarter of its channels in each of four lanes
+        uint2 w[D / 16];
+        uint32_t top = 0;
+        const int q = q0 + 8 * t + r;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            w[i] = make_uint2(0, 0);
+            if (q < p.nq)
+                w[i] = *reinterpret_cast<const uint2*>(p.Q + (bh * p.nq + q) * D + 64 * (i / 4) + 16 * c + 4 * (i % 4));
+            top = max(top, max(max(w[i].x & 0x7FFFu, (w[i].x >> 16) & 0x7FFFu),
+                               max(w[i].y & 0x7FFFu, (w[i].y >> 16) & 0x7FFFu)));
+        }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // 2^k brings the largest magnitude to [2^14, 2^15) (less below 2^-86)
+        const int k = min(14 + 127 - static_cast<int>(top >> 7), 100);
+        const float by = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const uint32_t x = y ? w[i].y : w[i].x;
+                const __half2 v = __floats2half2_rn(__uint_as_float(x << 16) * by,
+                                                    __uint_as_float(x & 0xFFFF0000u) * by);
+                st.q[i][t][y] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+        const float unit = __uint_as_float(static_cast<uint32_t>(127 - k) << 23) * p.scale_log2;
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            st.unit[t][y] = __shfl_sync(0xFFFFFFFFu, unit, 4 * (2 * c + y));
+            st.m[t][y] = -INFINITY;
+            st.l[t][y] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+            st.o[i][t][0] = st.o[i][t][1] = st.o[i][t][2] = st.o[i][t][3] = 0.f;
+    }
+
+    auto step = [&](const Group<D>& now, Group<D>& next) {
         if (key + WARPS * GROUP < end)
-            load_group(g, p, bh, key + WARPS * GROUP, end);
-        if (__any_sync(0xFFFFFFFFu, !(now.scale <= 128.f)))
-            group_step<D, true>(st, now, key, end, p.scale_log2);
+            load_group(next, p, at, bh, key + WARPS * GROUP, end);
+        if (__any_sync(0xFFFFFFFFu, lane >= 16 && !(now.scale <= 128.f)))
+            group_step<D, NT, true>(st, now, key, end);
         else
-            group_step<D, false>(st, now, key, end, p.scale_log2);
+            group_step<D, NT, false>(st, now, key, end);
+        key += WARPS * GROUP;
+    };
+    while (key < end) {
+        step(even, odd);
+        if (key < end)
+            step(odd, even);
     }
 #pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        st.l[y] += __shfl_xor_sync(0xFFFFFFFFu, st.l[y], 1);
-        st.l[y] += __shfl_xor_sync(0xFFFFFFFFu, st.l[y], 2);
-        if (c == 0) {
-            sm_m[warp][r + 8 * y] = st.m[y];
-            sm_l[warp][r + 8 * y] = st.l[y];
-        }
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            sm_o[warp][r + 8 * y][(D / 8) * (2 * c) + j] = st.o[j][2 * y];
-            sm_o[warp][r + 8 * y][(D / 8) * (2 * c + 1) + j] = st.o[j][2 * y + 1];
+        for (int y = 0; y < 2; ++y) {
+            const int q = 8 * t + 2 * c + y;
+            st.l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, st.l[t][y], 4);
+            st.l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, st.l[t][y], 8);
+            st.l[t][y] += __shfl_xor_sync(0xFFFFFFFFu, st.l[t][y], 16);
+            if (r == 0) {
+                sm_m[warp][q] = st.m[t][y];
+                sm_l[warp][q] = st.l[t][y];
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                *reinterpret_cast<float2*>(&sm_o[warp][q][(D / 8) * r + 2 * i]) =
+                    make_float2(st.o[i][t][y], st.o[i][t][2 + y]);
         }
-    }
     __syncthreads();
     for (int k = threadIdx.x; k < ROWS * D; k += WARPS * 32) {
         const int row = k / D, ch = k % D, q = q0 + row;
@@ -274,15 +384,15 @@ __global__ void __launch_bounds__(WARPS * 32) cache8_rows_kernel(const AttnParam
             l += sm_l[w][row] * f;
             o += sm_o[w][row][ch] * f;
         }
-        const long long at = bh * p.nq + q;
+        const long long row_at = bh * p.nq + q;
         if (p.splits > 1) {
-            p.part_o[(at * p.splits + split) * D + ch] = o;
+            p.part_o[(row_at * p.splits + split) * D + ch] = o;
             if (ch == 0)
-                p.part_ml[at * p.splits + split] = make_float2(m, l);
+                p.part_ml[row_at * p.splits + split] = make_float2(m, l);
         } else {
-            p.O[at * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+            p.O[row_at * D + ch] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
             if (p.lse && ch == 0)
-                p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+                p.lse[row_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
         }
     }
 }
@@ -326,7 +436,7 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
 constexpr int MIN_CHUNK = 256;
 constexpr int WHOLE = 512;  // as many keys as one block takes in less time than the join's launch
 constexpr int SMS = 148;
-constexpr int WANT_BLOCKS = SMS * 8;
+constexpr int WANT_BLOCKS = SMS * 16;
 constexpr int TILES_MIN_QUERIES = 33;  // more queries than this go to the many-query kernel
 constexpr double STEP_US = 0.9;        // a step of 64 keys of 256 queries
 constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
@@ -342,7 +452,7 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
 {
     Plan pl;
     pl.many = nq >= TILES_MIN_QUERIES;
-    const int rows = pl.many ? 256 : ROWS, unit = pl.many ? 64 : GROUP * WARPS;
+    const int rows = pl.many ? 256 : (nq <= COLS ? COLS : 2 * COLS), unit = pl.many ? 64 : GROUP * WARPS;
     pl.q_tiles = (nq + rows - 1) / rows;
     const long long tiles = static_cast<long long>(pl.q_tiles) * H * B;
     long long splits = 1;
@@ -475,10 +585,15 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
             return st;
     } else {
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
-        if (d == 64)
-            cache8_rows_kernel<64><<<grid, WARPS * 32, 0, cs>>>(p);
+        const bool one = nq <= COLS;
+        if (d == 64 && one)
+            cache8_rows_kernel<64, 1><<<grid, WARPS * 32, 0, cs>>>(p);
+        else if (d == 64)
+            cache8_rows_kernel<64, 2><<<grid, WARPS * 32, 0, cs>>>(p);
+        else if (one)
+            cache8_rows_kernel<128, 1><<<grid, WARPS * 32, 0, cs>>>(p);
         else
-            cache8_rows_kernel<128><<<grid, WARPS * 32, 0, cs>>>(p);
+            cache8_rows_kernel<128, 2><<<grid, WARPS * 32, 0, cs>>>(p);
         RA_CUDA_TRY(cudaGetLastError());
     }
     if (pl.splits == 1)
