@@ -3,8 +3,10 @@
 Argument marshalling only: every step of the computation runs in the library's
 CUDA kernels.  The C entry points are exposed under their own names
 (ra_build_mask, ra_attention_fwd, ...) taking plain integers / pointers, plus a
-thin torch-facing layer (Mask, build_mask, attention_fwd, attention_fwd_host)
-that passes tensor addresses and the current CUDA stream.
+thin torch-facing layer (Mask, build_mask, attention_fwd, attention_fwd_host, ...)
+that passes tensor addresses and the current CUDA stream.  The operators whose
+calls last microseconds (norm and rotation, the 8-bit ring) have that layer in a
+CPython extension, _torch_binding.so.
 
 There is no CPU fallback: importing this package fails loudly when the
 compiled library is missing (build it with
@@ -16,7 +18,6 @@ import contextlib
 import ctypes
 import math
 import os
-import struct
 from typing import NamedTuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +31,9 @@ LIB_PATH = os.path.join(_PKG, "libradattn_debug.so" if VARIANT == "debug" else "
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{os.path.basename(LIB_PATH)} is not built ({LIB_PATH}); run "
                       f"`python static_sparse_attention_b200/build.py{' --debug' if VARIANT == 'debug' else ''}`")
+
+if not os.path.exists(os.path.join(_PKG, "_torch_binding.so")):
+    raise ImportError("_torch_binding.so is not built; run `python static_sparse_attention_b200/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -158,19 +162,6 @@ def _refuse_capture(stream) -> None:
     with _allocating_on(stream, 0 if stream is None else _stream_handle(stream)):
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the cache's frame number is host state: a captured step would repeat it")
-
-
-def _workspace(torch, given, need: int, like, dev: int, stream, handle: int):
-    """The address of the caller's workspace, checked, or of one of `need` bytes, and the tensor that holds it."""
-    if given is not None:
-        if not given.is_contiguous() or given.get_device() != dev or given.numel() * given.element_size() < need:
-            raise ValueError(f"workspace must be a contiguous tensor of at least {need} bytes on the inputs' device")
-        return given.data_ptr(), given
-    if need == 0:
-        return None, None
-    with _allocating_on(stream, handle):
-        given = like.new_empty(need, dtype=torch.uint8)
-    return given.data_ptr(), given
 
 
 # ------------------------------------------------------------------- masks
@@ -411,69 +402,21 @@ def rope3d(frames: int, grid_h: int, grid_w: int, d: int, axes=None, base: float
     return Rope3D(*tables)
 
 
-# The C structs of a call, packed: a fraction of the time that building the ctypes
-# structures takes, which counts in calls of a few microseconds.
-_pack_rope = struct.Struct("PPPiiiiii").pack    # ra_rope
-_pack_rows = struct.Struct("PqqqiiP").pack      # ra_head_rows
-_pack_grads = struct.Struct("PPqqqP").pack      # ra_head_grads
+_binding = None
 
 
-def _current_device(torch, x) -> int:
-    """The index of the input's device, which has to be the current one (the library launches there)."""
-    dev = x.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current CUDA device")
-    return dev
+def _load_binding():
+    """The extension that checks and allocates the tensors of the operators below, bound to the loaded library."""
+    global _binding
+    if _binding is None:
+        import torch  # noqa: F401  (its libraries have to be loaded first)
 
-
-def _rope_arg(torch, rope, dev: int):
-    """The packed description of the tables (None without a rotation)."""
-    if rope is None:
-        return None
-    if len(rope) != 3:
-        raise ValueError("rope must be the tables of three axes")
-    t, h, w = rope
-    for x in rope:
-        if x.dtype is not torch.float32 or x.dim() != 3 or x.stride(2) != 1 or not x.is_contiguous() \
-                or x.get_device() != dev or x.shape[2] != 2:
-            raise ValueError("rope tables must be contiguous fp32 tensors [positions, pairs, 2] on the inputs' device")
-    frames, t_pairs, _ = t.shape
-    grid_h, h_pairs, _ = h.shape
-    grid_w, w_pairs, _ = w.shape
-    return _pack_rope(t.data_ptr(), h.data_ptr(), w.data_ptr(), frames, grid_h, grid_w, t_pairs, h_pairs, w_pairs)
-
-
-def _rows_arg(torch, name, x, heads, weight, d: int, dev: int):
-    """The packed description of a strided [B, n, heads, d] tensor and its norm weight."""
-    sb, sn, sh, sd = x.stride()
-    if x.dtype is not torch.bfloat16 or x.get_device() != dev or (sd != 1 and d != 1):
-        raise ValueError(f"{name} must be a bf16 tensor [B, n, H, d] with contiguous channels on the current CUDA device")
-    if weight is None:
-        return _pack_rows(x.data_ptr(), sb, sn, sh, heads, 0, 0)
-    fp32 = weight.dtype is torch.float32
-    if not (fp32 or weight.dtype is torch.bfloat16) or weight.shape != (d,) or weight.stride(0) != 1 \
-            or weight.get_device() != dev:
-        raise ValueError(f"the weight of {name} must be a contiguous bf16 or fp32 tensor [d] on {name}'s device")
-    return _pack_rows(x.data_ptr(), sb, sn, sh, heads, fp32, weight.data_ptr())
-
-
-def _output(torch, name, out, shape, like, dev: int, stream, handle: int):
-    """A contiguous bf16 output of that shape: the caller's, checked, or a new one."""
-    if out is None:
-        if stream is None:
-            return like.new_empty(shape)
-        with _allocating_on(stream, handle):
-            return like.new_empty(shape)
-    if out.dtype is not torch.bfloat16 or out.shape != shape or not out.is_contiguous() or out.get_device() != dev:
-        raise ValueError(f"{name} must be a contiguous bf16 tensor {shape} on the inputs' device")
-    return out
-
-
-def _check_qk(q, k):
-    if q.dim() != 4:
-        raise ValueError("q must be a tensor [B, n, H, d]")
-    if k is not None and (k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != q.shape[3]):
-        raise ValueError("k must be a tensor [B, n, Hk, d] with q's B, n and d")
+        from . import _torch_binding as module
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
+                      (ra_qk_norm_rope, ra_qk_norm_rope_bwd_workspace_bytes, ra_qk_norm_rope_bwd, ra_cache8_append,
+                       ra_cache8_attention_workspace_bytes, ra_cache8_attention)))
+        _binding = module
+    return _binding
 
 
 def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, frame0: int = 0, eps: float = 1e-6, q_out=None,
@@ -483,53 +426,13 @@ def qk_norm_rope(q, k=None, q_weight=None, k_weight=None, rope=None, frame0: int
     projection): returns (q, k) as bf16 [B, H, n, d], ready for attention_fwd.
 
     A weight (bf16 or fp32 [d]) turns the norm of its tensor on; rope (rope3d, or
-    three tables) the rotation, the first token being the first of frame `frame0`.
-    k may be left out (None is returned in its place)."""
-    import torch
-    dev = _current_device(torch, q)
-    _check_qk(q, k)
-    B, n, H, d = q.shape
-    handle = _stream_handle(stream)
-    rows_q = _rows_arg(torch, "q", q, H, q_weight, d, dev)
-    table = _rope_arg(torch, rope, dev)
-    q_out = _output(torch, "q_out", q_out, (B, H, n, d), q, dev, stream, handle)
-    rows_k = k_at = None
-    if k is not None:
-        Hk = k.shape[2]
-        rows_k = _rows_arg(torch, "k", k, Hk, k_weight, d, dev)
-        k_out = _output(torch, "k_out", k_out, (B, Hk, n, d), q, dev, stream, handle)
-        k_at = k_out.data_ptr()
-    elif k_weight is not None or k_out is not None:
-        raise ValueError("k_weight and k_out need k")
-    if n == 0:
-        return q_out, k_out
-    check(ra_qk_norm_rope(rows_q, rows_k, q_out.data_ptr(), k_at, B, n, d, table, frame0, eps, handle),
-          "ra_qk_norm_rope")
-    return q_out, k_out
-
-
-def _grads_arg(torch, name, weight, dy, dx, shape, like, dweight, dev: int, stream, handle: int):
-    """dx and dweight (new ones where they are not given) and the packed description of a tensor's gradients."""
-    B, n, H, d = shape
-    if dy.dtype is not torch.bfloat16 or dy.shape != (B, H, n, d) or not dy.is_contiguous() or dy.get_device() != dev:
-        raise ValueError(f"d{name}_out must be a contiguous bf16 tensor {(B, H, n, d)} on the inputs' device")
-    if dx is None:
-        with _allocating_on(stream, handle):
-            dx = like.new_empty(shape)
-    sb, sn, sh, sd = dx.stride()
-    if dx.dtype is not torch.bfloat16 or dx.get_device() != dev or dx.shape != shape or sd != 1:
-        raise ValueError(f"d{name} must be a bf16 tensor {tuple(shape)} with contiguous channels on the inputs' device")
-    if weight is None:
-        if dweight is not None:
-            raise ValueError(f"d{name}_weight needs a weight of {name}")
-        return dx, None, _pack_grads(dy.data_ptr(), dx.data_ptr(), sb, sn, sh, 0)
-    if dweight is None:
-        with _allocating_on(stream, handle):
-            dweight = like.new_empty(d, dtype=torch.float32)
-    elif dweight.dtype is not torch.float32 or dweight.shape != (d,) or not dweight.is_contiguous() \
-            or dweight.get_device() != dev:
-        raise ValueError(f"d{name}_weight must be a contiguous fp32 tensor [d] on the inputs' device")
-    return dx, dweight, _pack_grads(dy.data_ptr(), dx.data_ptr(), sb, sn, sh, dweight.data_ptr())
+    a tuple of three tables) the rotation, the first token being the first of frame
+    `frame0`.  k may be left out (None is returned in its place)."""
+    r = (_binding or _load_binding()).qk_norm_rope(q, k, q_weight, k_weight, rope, frame0, eps, q_out, k_out,
+                                                    None if stream is None else _stream_handle(stream))
+    if type(r) is int:
+        check(r, "ra_qk_norm_rope")
+    return r
 
 
 def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=None, frame0: int = 0, eps: float = 1e-6,
@@ -539,59 +442,16 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight=None, k_weight=None, rope=No
     [B, n, H, d] (given ones may be strided, such as slices of one packed gradient)
     and fp32 [d] for each weight (None without one).  q, k, the weights, rope,
     frame0 and eps as in the forward call; k and dk_out may both be None."""
-    import torch
-    dev = _current_device(torch, q)
-    _check_qk(q, k)
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out go together")
-    shape = q.shape
-    B, n, H, d = shape
-    handle = _stream_handle(stream)
-    rows_q = _rows_arg(torch, "q", q, H, q_weight, d, dev)
-    table = _rope_arg(torch, rope, dev)
-    dq, dq_weight, grads_q = _grads_arg(torch, "q", q_weight, dq_out, dq, shape, q, dq_weight, dev, stream, handle)
-    rows_k = grads_k = None
-    if k is not None:
-        rows_k = _rows_arg(torch, "k", k, k.shape[2], k_weight, d, dev)
-        dk, dk_weight, grads_k = _grads_arg(torch, "k", k_weight, dk_out, dk, k.shape, q, dk_weight, dev, stream, handle)
-    elif k_weight is not None or dk is not None or dk_weight is not None:
-        raise ValueError("k_weight, dk and dk_weight need k")
-    if n == 0:
-        for w in (dq_weight, dk_weight):
-            if w is not None:
-                with _allocating_on(stream, handle):
-                    w.zero_()
-        return dq, dk, dq_weight, dk_weight
-    need = ra_qk_norm_rope_bwd_workspace_bytes(d) if dq_weight is not None or dk_weight is not None else 0
-    at, workspace = _workspace(torch, workspace, need, q, dev, stream, handle)
-    check(ra_qk_norm_rope_bwd(rows_q, rows_k, grads_q, grads_k, B, n, d, table, frame0, eps, at, need, handle),
-          "ra_qk_norm_rope_bwd")
-    return dq, dk, dq_weight, dk_weight
+    r = (_binding or _load_binding()).qk_norm_rope_bwd(q, k, dq_out, dk_out, q_weight, k_weight, rope, frame0, eps, dq,
+                                                        dk, dq_weight, dk_weight, workspace,
+                                                        None if stream is None else _stream_handle(stream))
+    if type(r) is int:
+        check(r, "ra_qk_norm_rope_bwd")
+    return r
 
 
 # ------------------------------------------------------- 8-bit key/value ring
 CACHE8_BLOCK = 64  # tokens of a frame that share a scale
-
-
-def _ring_shape(torch, k8, v8, k_scale, v_scale, dev: int):
-    """(B, H, d, s, W) of an 8-bit ring, checked."""
-    shape, scales = k8.shape, k_scale.shape
-    if len(shape) != 4 or len(scales) != 4:
-        raise ValueError("k8 must be [B, H, W * s, d] and k_scale [B, H, W, ceil(s / 64)]")
-    B, H, rows, d = shape
-    W = scales[2]
-    s = rows // W if W else 0
-    if s < 1 or rows != s * W or scales != (B, H, W, -(-s // CACHE8_BLOCK)):
-        raise ValueError("k_scale must be [B, H, W, ceil(s / 64)] for k8 [B, H, W * s, d]")
-    for codes in (k8, v8):
-        if codes.dtype is not torch.float8_e4m3fn or codes.shape != shape or not codes.is_contiguous() \
-                or codes.get_device() != dev:
-            raise ValueError(f"k8 and v8 must be contiguous float8_e4m3fn tensors {tuple(shape)} on the inputs' device")
-    for scale in (k_scale, v_scale):
-        if scale.dtype is not torch.float32 or scale.shape != scales or not scale.is_contiguous() \
-                or scale.get_device() != dev:
-            raise ValueError(f"k_scale and v_scale must be contiguous fp32 tensors {tuple(scales)} on the inputs' device")
-    return B, H, d, s, W
 
 
 def cache8_append(k, v, k8, v8, k_scale, v_scale, frame: int, k_weight=None, rope=None, eps: float = 1e-6,
@@ -603,16 +463,9 @@ def cache8_append(k, v, k8, v8, k_scale, v_scale, frame: int, k_weight=None, rop
     k, v: bf16 [B, frames * s, H, d], any strides with contiguous channels.  A
     k_weight (bf16 or fp32 [d]) norms the keys, rope (tables whose grid is one
     frame's) rotates them on the way."""
-    import torch
-    dev = _current_device(torch, k)
-    B, H, d, s, W = _ring_shape(torch, k8, v8, k_scale, v_scale, dev)
-    shape = k.shape
-    n = shape[1] if len(shape) == 4 else -1
-    if shape != (B, n, H, d) or v.shape != shape or n % s:
-        raise ValueError(f"k and v must have shape [{B}, frames * {s}, {H}, {d}]")
-    check(ra_cache8_append(_rows_arg(torch, "k", k, H, k_weight, d, dev), _rows_arg(torch, "v", v, H, None, d, dev), B,
-                           n // s, d, s, W, frame, _rope_arg(torch, rope, dev), eps, k8.data_ptr(), v8.data_ptr(),
-                           k_scale.data_ptr(), v_scale.data_ptr(), _stream_handle(stream)), "ra_cache8_append")
+    check((_binding or _load_binding()).cache8_append(k, v, k8, v8, k_scale, v_scale, frame, k_weight, rope, eps,
+                                                       None if stream is None else _stream_handle(stream)),
+          "ra_cache8_append")
 
 
 def cache8_attention(q, k8, v8, k_scale, v_scale, held: int, key_counts=None, scale: float | None = None, out=None,
@@ -620,36 +473,11 @@ def cache8_attention(q, k8, v8, k_scale, v_scale, held: int, key_counts=None, sc
     """Attention of q (bf16 [B, H, nq, d], nq >= 1) over the frames in slots 0 ..
     held - 1 of an 8-bit ring (see cache8_append).  key_counts (int32 [B]) limits
     each batch element to its first rows; a query without keys gets 0 (lse -inf)."""
-    import torch
-    dev = _current_device(torch, q)
-    B, H, d, s, W = _ring_shape(torch, k8, v8, k_scale, v_scale, dev)
-    shape = q.shape
-    nq = shape[2] if len(shape) == 4 else -1
-    if q.dtype is not torch.bfloat16 or shape != (B, H, nq, d) or not q.is_contiguous():
-        raise ValueError(f"q must be a contiguous bf16 tensor [{B}, {H}, nq, {d}]")
-    counts_at = lse_at = None
-    if key_counts is not None:
-        if key_counts.dtype is not torch.int32 or key_counts.shape != (B,) or not key_counts.is_contiguous() \
-                or key_counts.get_device() != dev:
-            raise ValueError(f"key_counts must be a contiguous int32 tensor [{B}] on the inputs' device")
-        counts_at = key_counts.data_ptr()
-    if lse is not None:
-        if lse.dtype is not torch.float32 or lse.shape != (B, H, nq) or not lse.is_contiguous() \
-                or lse.get_device() != dev:
-            raise ValueError("lse must be a contiguous fp32 tensor [B, H, nq] on the inputs' device")
-        lse_at = lse.data_ptr()
-    handle = _stream_handle(stream)
-    out = _output(torch, "out", out, (B, H, nq, d), q, dev, stream, handle)
-    if nq == 0:
-        return out
-    need = ctypes.c_size_t()
-    check(ra_cache8_attention_workspace_bytes(B, H, d, nq, s, W, held, ctypes.byref(need)), "ra_cache8_attention")
-    at, workspace = _workspace(torch, workspace, need.value, q, dev, stream, handle)
-    check(ra_cache8_attention(q.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                              out.data_ptr(), B, H, d, nq, s, W, held, counts_at,
-                              1.0 / math.sqrt(d) if scale is None else scale, lse_at, at, need.value, handle),
-          "ra_cache8_attention")
-    return out
+    r = (_binding or _load_binding()).cache8_attention(q, k8, v8, k_scale, v_scale, held, key_counts, scale, out, lse,
+                                                        workspace, None if stream is None else _stream_handle(stream))
+    if type(r) is int:
+        check(r, "ra_cache8_attention")
+    return r
 
 
 class SwcCache8:

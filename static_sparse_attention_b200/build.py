@@ -8,13 +8,19 @@
 they derive from their inputs and record a failure in the device error word
 (RA_ERR_DEVICE_BOUNDS) instead of making the access.  The binding loads it when
 RA_LIBRARY_VARIANT=debug is set.
+
+Both also build _torch_binding.so (g++, torch's headers), the tensor checks of the
+operators whose calls last microseconds; it takes the entry points' addresses from
+the package and is not linked to the library.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -53,8 +59,30 @@ def nvcc() -> str:
     return "nvcc"
 
 
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_torch_binding.so")
+
+
+def build_binding(force: bool = False) -> str:
+    deps = (BINDING_SRC, os.path.join(INCLUDE, "radattn.h"))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+        return BINDING
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    tmp = BINDING + f".tmp{os.getpid()}"
+    subprocess.check_call([
+        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+        "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+        "-I", sysconfig.get_path("include"), "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
+        "-L", os.path.join(torch, "lib"),
+        *("-l" + lib for lib in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda"))])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
+    build_binding(force)
     if not force and not _stale(lib):
         return lib
     tmp = lib + f".tmp{os.getpid()}"
