@@ -7,13 +7,13 @@
 //                   group owns row t (TMEM lane t); per step reads S, keeps the
 //                   running maximum and sum, writes P (bf16) back over S; at the end
 //                   the epilogue.
-//   warp 13         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
+//   warp 14         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
 //                   are contiguous) into a ring of shared memory, RAW steps ahead; its
 //                   lanes turn the rows' scales into the factors of the conversion.
 //   warps 8-11      convert: codes become code * scale in bf16 -- exactly, see
 //                   ra_cache8.cuh -- in the MMA's 128-byte swizzle, in a ring of K
 //                   stages and one of V stages.
-//   warp 12         MMA: allocates TMEM; one elected lane issues, for both tiles,
+//   warps 12, 13    MMA of tile 0 and 1 (12 allocates TMEM): one elected lane issues
 //                   S_h = Q K_h^T (N = 64) into S buffer h % 2 and O += P_h V_h, in
 //                   the order S_0, S_1, PV_0, S_2, PV_1, ...
 // Two query tiles share one conversion: per step it costs about 5.5 integer and
@@ -56,7 +56,7 @@ namespace {
 constexpr int STEP = 64;           // keys of a step
 constexpr int TILE_ROWS = 128;     // queries of a tile
 constexpr int THREADS = 512;
-constexpr int CONVERT_WARP = 8, MMA_WARP = 12, FETCH_WARP = 13;
+constexpr int CONVERT_WARP = 8, MMA_WARP = 12, FETCH_WARP = 14;  // MMA: 12 and 13, one for each tile
 // Registers a thread of each warpgroup keeps of the 128 that the block is launched
 // with: the softmax holds 64 scores, P and its sums.
 constexpr int SOFTMAX_REGS = 160, CONVERT_REGS = 112, MMA_REGS = 72;
@@ -91,7 +91,7 @@ struct Layout {
     static constexpr int FACTOR_OFF = RAW_OFF + RAW * 2 * RAW_TILE;
     static constexpr int FACTORS = 2 * STEP + 4;                // words: of K's rows, of V's rows, the TWO flag
     static constexpr int BAR_OFF = FACTOR_OFF + RAW * FACTORS * 4;
-    static constexpr int SMEM = BAR_OFF + 256;
+    static constexpr int SMEM = BAR_OFF + 272;
     static_assert(SMEM <= 227 * 1024, "one block's shared memory");
 };
 
@@ -105,16 +105,17 @@ enum : int {
     B_S_FULL = 20,     // + 2 * tile + buffer
     B_P_FULL = 24,     // + 2 * tile + buffer
     B_PV_DONE = 28,    // + tile
-    B_O_FINAL = 30,
-    B_COUNT = 31
+    B_O_FINAL = 30,    // + tile
+    B_COUNT = 32
 };
 constexpr int CONVERT_WARPS = 4;
 
-// Arrivals that complete a phase of barrier i: the convert warps, the threads of a
-// softmax warpgroup, or one thread (the MMA's commits, the fetch).
-__host__ __device__ constexpr uint32_t arrivals(int i)
+// Arrivals that complete a phase of barrier i: the convert warps, a commit for each
+// tile, the threads of a softmax warpgroup, or one thread (a tile's commit, the fetch).
+__device__ __forceinline__ uint32_t arrivals(int i, int tiles)
 {
     return i < B_K_EMPTY || (i >= B_RAW_EMPTY && i < B_S_FULL) ? CONVERT_WARPS
+           : i < B_RAW_FULL                                    ? tiles
            : i >= B_P_FULL && i < B_PV_DONE                    ? 128u
                                                                : 1u;
 }
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         if (sbase & 1023u)  // the swizzled tiles need 1024-byte alignment: record it, run nothing
             report_timeout(wc, SITE_SMEM_ALIGN);
         for (int i = 0; i < B_COUNT; ++i)
-            mbar_init(bar(i), arrivals(i));
+            mbar_init(bar(i), arrivals(i, tiles));
         fence_barrier_init();
     }
     if (warp == MMA_WARP) {
@@ -297,11 +298,12 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     if (warp >= MMA_WARP) {
         // ----------------------------------------------------------------- MMA
         shed_registers<MMA_REGS>();
-        if (warp == MMA_WARP && n > 0) {
+        if (warp < FETCH_WARP && warp - MMA_WARP < tiles && n > 0) {
+            const int t = warp - MMA_WARP;
             const bool leader = elect_one();
             constexpr uint32_t idesc_s = idesc_bf16_f32(TILE_ROWS, STEP, 0, 0);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(TILE_ROWS, D, 0, 1);
-            const uint64_t q_desc = smem_desc_sw128(sbase, 16, 1024);
+            const uint64_t q_desc = smem_desc_sw128(sbase + t * L::Q_TILE, 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(sbase + L::K_OFF, 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(sbase + L::V_OFF, L::KV_CHUNK, 1024);  // V as MN-major B
             auto wait_all = [&](uint32_t bb, uint32_t parity, int site) {
@@ -315,50 +317,43 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                         break;
                     fence_proxy_async_smem();
                     tc_fence_after();
+                    // behind the P V of step hh - 2, which reads this buffer (see the header)
+                    if (hh >= 2 && leader)
+                        tmem_shift_down(tmem + s_col(t, hh & 1));
                     const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
-                    for (int t = 0; t < tiles; ++t) {
-                        // behind the P V of step hh - 2, which reads this buffer (see the header)
-                        if (hh >= 2 && leader)
-                            tmem_shift_down(tmem + s_col(t, hh & 1));
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint64_t ad =
-                                desc_add(q_desc, t * L::Q_TILE + (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
-                            const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
-                            mma_ss(leader, tmem + s_col(t, hh & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
-                        }
-                        if (leader)
-                            mma_commit(bar(B_S_FULL + 2 * t + (hh & 1)));
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t ad = desc_add(q_desc, (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
+                        const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
+                        mma_ss(leader, tmem + s_col(t, hh & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
                     }
-                    if (leader)
+                    if (leader) {
+                        mma_commit(bar(B_S_FULL + 2 * t + (hh & 1)));
                         mma_commit(bar(B_K_EMPTY + st));
+                    }
                 }
                 if (hh >= 1) {
                     const int j = hh - 1, st = j % L::STAGES, buf = j & 1;
                     const uint64_t vd = desc_add(v_desc, st * L::KV_TILE);
-                    for (int t = 0; t < tiles; ++t) {
-                        if (t == 0 && !(ok = wait_all(bar(B_V_FULL + st), (j / L::STAGES) & 1, SITE_V_FULL)))
-                            break;
-                        if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (j >> 1) & 1, SITE_P_FULL)))
-                            break;
-                        if (t == 0)
-                            fence_proxy_async_smem();
-                        tc_fence_after();
+                    if (!(ok = wait_all(bar(B_V_FULL + st), (j / L::STAGES) & 1, SITE_V_FULL)) ||
+                        !(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (j >> 1) & 1, SITE_P_FULL)))
+                        break;
+                    fence_proxy_async_smem();
+                    tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < STEP / 16; ++kk)
-                            mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048),
-                                   idesc_pv, (j > 0 || kk > 0) ? 1u : 0u);
-                        if (leader)
-                            mma_commit(bar(B_PV_DONE + t));
-                    }
-                    if (ok && leader)
+                    for (int kk = 0; kk < STEP / 16; ++kk)
+                        mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048), idesc_pv,
+                               (j > 0 || kk > 0) ? 1u : 0u);
+                    if (leader) {
+                        mma_commit(bar(B_PV_DONE + t));
                         mma_commit(bar(B_V_EMPTY + st));
+                    }
                 }
             }
             if (leader)
-                mma_commit(bar(B_O_FINAL));
+                mma_commit(bar(B_O_FINAL + t));
             // Every MMA issued by the elected lane has completed once O_FINAL fires.
-            drain_wait(bar(B_O_FINAL), 0, p.timeout_ns);
+            drain_wait(bar(B_O_FINAL + t), 0, p.timeout_ns);
         } else if (warp == FETCH_WARP && n > 0) {
             // ----------------------------------------------------------- fetch
             const int lane = threadIdx.x & 31;
@@ -552,7 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
 
         // ------------------------------------------------------------ epilogue
         if (n > 0 && ok)
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_O_FINAL), 0, wc, SITE_O_FINAL));
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_O_FINAL + t), 0, wc, SITE_O_FINAL));
         tc_fence_after();
         if (ok && !*abort_flag) {
             const long long at = bh * p.nq + row;
