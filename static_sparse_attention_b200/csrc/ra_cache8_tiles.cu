@@ -55,12 +55,12 @@ namespace {
 
 constexpr int STEP = 64;           // keys of a step
 constexpr int TILE_ROWS = 128;     // queries of a tile
-constexpr int THREADS = 512;
-constexpr int CONVERT_WARP = 8, MMA_WARP = 12, FETCH_WARP = 14;  // MMA: 12 and 13, one for each tile
+constexpr int THREADS = 640;
+constexpr int CONVERT_WARP = 8, MMA_WARP = 16, FETCH_WARP = 18;  // MMA: 16 and 17, one for each tile
 // Registers a thread of each warpgroup keeps of the 128 that the block is launched
 // with: the softmax holds 64 scores, P and its sums.
-constexpr int SOFTMAX_REGS = 160, CONVERT_REGS = 112, MMA_REGS = 72;
-static_assert(2 * SOFTMAX_REGS + CONVERT_REGS + MMA_REGS <= 4 * 128, "the split draws on the block's own registers");
+constexpr int SOFTMAX_REGS = 152, CONVERT_REGS = 56, MMA_REGS = 64;
+static_assert(2 * SOFTMAX_REGS + 2 * CONVERT_REGS + MMA_REGS <= 5 * 96, "the split draws on the block's own registers");
 constexpr uint32_t TMEM_COLS = 512;
 // TMEM columns of a tile: S / P buffers 0 and 1 (64 fp32 columns each), then O.
 __host__ __device__ constexpr uint32_t tile_col(int t) { return 256u * static_cast<uint32_t>(t); }
@@ -108,7 +108,7 @@ enum : int {
     B_O_FINAL = 30,    // + tile
     B_COUNT = 32
 };
-constexpr int CONVERT_WARPS = 4;
+constexpr int CONVERT_WARPS = 8;
 
 // Arrivals that complete a phase of barrier i: the convert warps, a commit for each
 // tile, the threads of a softmax warpgroup, or one thread (a tile's commit, the fetch).
