@@ -15,7 +15,7 @@
 //                   stages and one of V stages.
 //   warps 12, 13    MMA of tile 0 and 1 (12 allocates TMEM): one elected lane issues
 //                   S_h = Q K_h^T (N = 64) into S buffer h % 2 and O += P_h V_h, in
-//                   the order S_0, S_1, PV_0, S_2, PV_1, ...
+//                   the order S_0, S_1, PV_0, S_2, PV_1, S_3, ...
 // Two query tiles share one conversion: per step it costs about 5.5 integer and
 // multiply instructions for two codes, 1400 warp instructions for 64 keys of 128
 // channels, against 2900 for the softmax of 2 x 128 x 64 scores and 1280 clocks of
@@ -309,46 +309,57 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             auto wait_all = [&](uint32_t bb, uint32_t parity, int site) {
                 return __all_sync(0xFFFFFFFFu, mbar_wait(bb, parity, wc, site)) != 0;
             };
+            // S of step h, whose K has been waited for
+            auto issue_s = [&](int h) {
+                const int st = h % L::STAGES;
+                // behind the P V of step h - 2, which reads this buffer (see the header)
+                if (h >= 2 && leader)
+                    tmem_shift_down(tmem + s_col(t, h & 1));
+                const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t ad = desc_add(q_desc, (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
+                    const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
+                    mma_ss(leader, tmem + s_col(t, h & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+                }
+                if (leader) {
+                    mma_commit(bar(B_S_FULL + 2 * t + (h & 1)));
+                    mma_commit(bar(B_K_EMPTY + st));
+                }
+            };
+            auto wait_k = [&](int h) {
+                return wait_all(bar(B_K_FULL + h % L::STAGES), (h / L::STAGES) & 1, SITE_K_FULL);
+            };
             bool ok = true;
-            for (int hh = 0; ok && hh <= n; ++hh) {
-                if (hh < n) {
-                    const int st = hh % L::STAGES;
-                    if (!(ok = wait_all(bar(B_K_FULL + st), (hh / L::STAGES) & 1, SITE_K_FULL)))
-                        break;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    // behind the P V of step hh - 2, which reads this buffer (see the header)
-                    if (hh >= 2 && leader)
-                        tmem_shift_down(tmem + s_col(t, hh & 1));
-                    const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
+            for (int h = 0; ok && h < min(n, 2); ++h) {
+                if (!(ok = wait_k(h)))
+                    break;
+                fence_proxy_async_smem();
+                tc_fence_after();
+                issue_s(h);
+            }
+            for (int h = 0; ok && h < n; ++h) {
+                // V of this step and K of the step after next first, so that nothing
+                // stands between P and the two products behind it
+                const int st = h % L::STAGES, buf = h & 1;
+                if (!(ok = wait_all(bar(B_V_FULL + st), (h / L::STAGES) & 1, SITE_V_FULL)) ||
+                    !(ok = h + 2 >= n || wait_k(h + 2)))
+                    break;
+                fence_proxy_async_smem();
+                if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (h >> 1) & 1, SITE_P_FULL)))
+                    break;
+                tc_fence_after();
+                const uint64_t vd = desc_add(v_desc, st * L::KV_TILE);
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t ad = desc_add(q_desc, (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
-                        const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
-                        mma_ss(leader, tmem + s_col(t, hh & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
-                    }
-                    if (leader) {
-                        mma_commit(bar(B_S_FULL + 2 * t + (hh & 1)));
-                        mma_commit(bar(B_K_EMPTY + st));
-                    }
+                for (int kk = 0; kk < STEP / 16; ++kk)
+                    mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048), idesc_pv,
+                           (h > 0 || kk > 0) ? 1u : 0u);
+                if (leader) {
+                    mma_commit(bar(B_PV_DONE + t));
+                    mma_commit(bar(B_V_EMPTY + st));
                 }
-                if (hh >= 1) {
-                    const int j = hh - 1, st = j % L::STAGES, buf = j & 1;
-                    const uint64_t vd = desc_add(v_desc, st * L::KV_TILE);
-                    if (!(ok = wait_all(bar(B_V_FULL + st), (j / L::STAGES) & 1, SITE_V_FULL)) ||
-                        !(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (j >> 1) & 1, SITE_P_FULL)))
-                        break;
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < STEP / 16; ++kk)
-                        mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048), idesc_pv,
-                               (j > 0 || kk > 0) ? 1u : 0u);
-                    if (leader) {
-                        mma_commit(bar(B_PV_DONE + t));
-                        mma_commit(bar(B_V_EMPTY + st));
-                    }
-                }
+                if (h + 2 < n)
+                    issue_s(h + 2);
             }
             if (leader)
                 mma_commit(bar(B_O_FINAL + t));
