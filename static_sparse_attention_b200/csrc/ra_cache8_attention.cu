@@ -414,15 +414,28 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
 #pragma unroll
     for (int i = 16; i >= 1; i >>= 1)
         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, i));
+    // 32 splits' factors at a time, one a lane; then their O, several loads in flight
     float l = 0.f, o[D / 32] = {};
-    for (int k = 0; k < n; ++k) {
-        const float2 x = ml[k];
-        const float f = x.x == -INFINITY ? 1.f : exp2_fast(x.x - m);
-        l += x.y * f;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+        float f = 0.f;
+        if (k0 + lane < n) {
+            const float2 x = ml[k0 + lane];
+            f = x.x == -INFINITY ? 1.f : exp2_fast(x.x - m);  // 1: its sums are 0 or NaN
+            l += x.y * f;
+        }
+        const float* part = p.part_o + (at * p.splits + k0) * D + lane;
+        const int here = min(32, n - k0);
+#pragma unroll 8
+        for (int k = 0; k < here; ++k) {
+            const float by = __shfl_sync(0xFFFFFFFFu, f, k);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            o[i] += p.part_o[(at * p.splits + k) * D + i * 32 + lane] * f;
+            for (int i = 0; i < D / 32; ++i)
+                o[i] = fmaf(part[k * D + i * 32], by, o[i]);
+        }
     }
+#pragma unroll
+    for (int i = 16; i >= 1; i >>= 1)
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, i);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
         p.O[at * D + i * 32 + lane] = __float2bfloat16_rn(l == 0.f ? 0.f : o[i] / l);
@@ -430,14 +443,21 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
         p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-// How the work is cut.  Few queries: ranges of at least MIN_CHUNK keys, enough
-// blocks for every SM.  Many: the number of ranges with the least estimated time,
-// counted in steps of 64 keys of the 256-query kernel (one block an SM).
-constexpr int MIN_CHUNK = 256;
+// How the work is cut.  Few queries: ranges of at least MIN_CHUNK keys, as many as
+// fill the SMs once, or several times where the ranges stay above LONG_CHUNK (batches
+// of unequal lengths balance better).  Many: the number of ranges with the least
+// estimated time, counted in steps of 64 keys of the 256-query kernel (one block an
+// SM).
+constexpr int MIN_CHUNK = 256, LONG_CHUNK = 1024;
 constexpr int WHOLE = 512;  // as many keys as one block takes in less time than the join's launch
 constexpr int SMS = 148;
+constexpr int ONE_WAVE = SMS * 3;
 constexpr int WANT_BLOCKS = SMS * 16;
-constexpr int TILES_MIN_QUERIES = 33;  // more queries than this go to the many-query kernel
+// More than 16 queries go to the many-query kernel (24 heads of 128, 2048 keys: 24 us
+// against 19 at 17 queries; at 16 the two are equal), except over so few keys that
+// the few-query kernel takes them in one go with blocks to spare (256 keys, 24 heads
+// of 64, 128 queries: 9.5 against 10.4 us; twice the blocks: 14.5 against 20.7).
+constexpr int FEW_BLOCKS = 192;
 constexpr double STEP_US = 0.9;        // a step of 64 keys of 256 queries
 constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
 constexpr double JOIN_BYTES_PER_US = 5e6;
@@ -451,7 +471,7 @@ struct Plan {
 Plan plan_of(int B, int H, int d, int nq, int nk)
 {
     Plan pl;
-    pl.many = nq >= TILES_MIN_QUERIES;
+    pl.many = nq > 2 * COLS && !(nk <= WHOLE && static_cast<long long>((nq + 2 * COLS - 1) / (2 * COLS)) * H * B <= FEW_BLOCKS);
     const int rows = pl.many ? 256 : (nq <= COLS ? COLS : 2 * COLS), unit = pl.many ? 64 : GROUP * WARPS;
     pl.q_tiles = (nq + rows - 1) / rows;
     const long long tiles = static_cast<long long>(pl.q_tiles) * H * B;
@@ -470,7 +490,10 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
             }
         }
     } else {
-        splits = (WANT_BLOCKS + tiles - 1) / tiles;
+        const long long one_wave = (ONE_WAVE + tiles - 1) / tiles, waves = (WANT_BLOCKS + tiles - 1) / tiles;
+        const long long long_chunks = nk / LONG_CHUNK;
+        splits = waves < long_chunks ? waves : long_chunks;
+        splits = splits > one_wave ? splits : one_wave;
         const long long most = nk <= WHOLE ? 1 : (static_cast<long long>(nk) + MIN_CHUNK - 1) / MIN_CHUNK;
         splits = splits < most ? splits : most;
         splits = splits < 1 ? 1 : splits;

@@ -277,15 +277,25 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         tmem_relinquish();
     }
     // Q, zeros behind the last query, in the order of channels that K has
-    for (int i = threadIdx.x; i < tiles * TILE_ROWS * (D / 8); i += THREADS) {
-        const int row = i / (D / 8), unit = i % (D / 8);
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (q0 + row < p.nq)
-            v = *reinterpret_cast<const uint4*>(p.Q + (bh * p.nq + q0 + row) * D + unit * 8);
-        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x5410),
-                       __byte_perm(v.z, v.w, 0x7632));
-        uint8_t* at = smem + (row / TILE_ROWS) * L::Q_TILE + (unit / 8) * L::Q_CHUNK + (row % TILE_ROWS) * 128;
-        *reinterpret_cast<uint4*>(at + (((unit % 8) ^ (row & 7)) << 4)) = v;
+    constexpr int UNITS = D / 8, LOADS = 4;  // 16-byte units of a row; loads in flight
+    for (int i0 = threadIdx.x; i0 < tiles * TILE_ROWS * UNITS; i0 += THREADS * LOADS) {
+        uint4 v[LOADS];
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int i = i0 + THREADS * j, row = i / UNITS;
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (row < tiles * TILE_ROWS && q0 + row < p.nq)
+                v[j] = *reinterpret_cast<const uint4*>(p.Q + (bh * p.nq + q0 + row) * D + i % UNITS * 8);
+        }
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int i = i0 + THREADS * j, row = i / UNITS, unit = i % UNITS;
+            uint8_t* at = smem + (row / TILE_ROWS) * L::Q_TILE + (unit / 8) * L::Q_CHUNK + (row % TILE_ROWS) * 128;
+            if (row < tiles * TILE_ROWS)
+                *reinterpret_cast<uint4*>(at + (((unit % 8) ^ (row & 7)) << 4)) =
+                    make_uint4(__byte_perm(v[j].x, v[j].y, 0x5410), __byte_perm(v[j].x, v[j].y, 0x7632),
+                               __byte_perm(v[j].z, v[j].w, 0x5410), __byte_perm(v[j].z, v[j].w, 0x7632));
+        }
     }
     fence_proxy_async_smem();
     tc_fence_before();
