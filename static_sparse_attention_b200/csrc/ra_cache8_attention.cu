@@ -289,6 +289,8 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kerne
         return;  // the join does not read this split
     const int end = min(begin + p.chunk, count);
     const int q0 = q_tile * ROWS;
+    if (p.splits > 1)
+        let_next_launch();
 
     // two groups in registers, taken in turn: one on its way while the other is computed
     Group<D> even, odd;
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kerne
 template <int D>
 __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, long long rows)
 {
+    wait_for_previous();
     const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (at >= rows)
@@ -621,10 +624,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     }
     if (pl.splits == 1)
         return RA_OK;
-    const unsigned joins = static_cast<unsigned>((rows + 3) / 4);
-    if (d == 64)
-        cache8_join_kernel<64><<<joins, 128, 0, cs>>>(p, rows);
-    else
-        cache8_join_kernel<128><<<joins, 128, 0, cs>>>(p, rows);
-    return cuda_fail(cudaGetLastError(), "cache8_join_kernel launch");
+    const dim3 joins(static_cast<unsigned>((rows + 3) / 4));
+    return launch_behind("cache8_join_kernel launch", d == 64 ? cache8_join_kernel<64> : cache8_join_kernel<128>, joins,
+                         dim3(128), cs, p, rows);
 }

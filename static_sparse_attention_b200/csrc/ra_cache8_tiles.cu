@@ -263,6 +263,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     const int q0 = q_tile * 2 * TILE_ROWS;
     const int tiles = p.nq - q0 > TILE_ROWS ? 2 : 1;
     WaitCtl wc{abort_flag, p.err, p.timeout_ns};
+    if (p.splits > 1)
+        let_next_launch();
 
     if (threadIdx.x == 0) {
         *abort_flag = *reinterpret_cast<volatile int*>(p.err) != 0 ? 1 : 0;

@@ -85,6 +85,29 @@ inline long long extent(long long sb, long long sn, long long sh, int B, int n, 
 
 struct RopeArgs;
 
+// Launch a kernel that reads what the kernel before it on the stream has written,
+// and begins with wait_for_previous(): its blocks may be set up while the other's
+// last ones run (the other calls let_next_launch(); without it, when it ends).
+template <typename... Args>
+ra_status launch_behind(const char* what, void (*kernel)(Args...), dim3 grid, dim3 block, cudaStream_t stream, Args... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = block;
+    config.stream = stream;
+    config.attrs = &attr;
+    config.numAttrs = 1;
+    return cuda_fail(cudaLaunchKernelEx(&config, kernel, args...), what);
+}
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
+
 // Check a rope description against n tokens from frame frame0 on and fill the
 // kernels' arguments (no rotation when rope is NULL).
 ra_status rope_args(const ra_rope* rope, int frame0, int n, int d, RopeArgs* out);

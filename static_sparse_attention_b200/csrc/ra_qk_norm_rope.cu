@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
 {
     constexpr int LPR = D / 8, TOKENS = THREADS / LPR;
     const Rows& t = p.t[blockIdx.y];
+    let_next_launch();
     const int sub = threadIdx.x % LPR;
     const int tok = static_cast<int>(threadIdx.x) / LPR;
     const bool norm = t.weight != nullptr;
@@ -195,6 +196,7 @@ template <int D>
 __global__ void __launch_bounds__(1024) weight_grad_kernel(const Params p, int blocks)
 {
     constexpr int G = 1024 / D;
+    wait_for_previous();
     const Rows& t = p.t[blockIdx.x];
     if (!t.dw_part)
         return;
@@ -562,9 +564,6 @@ extern "C" ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_ro
     RA_CUDA_TRY(cudaGetLastError());
     if (!weights)
         return RA_OK;
-    if (d == 64)
-        weight_grad_kernel<64><<<k ? 2 : 1, 1024, 0, cs>>>(p, blocks);
-    else
-        weight_grad_kernel<128><<<k ? 2 : 1, 1024, 0, cs>>>(p, blocks);
-    return cuda_fail(cudaGetLastError(), "weight_grad_kernel launch");
+    return launch_behind("weight_grad_kernel launch", d == 64 ? weight_grad_kernel<64> : weight_grad_kernel<128>,
+                         dim3(k ? 2 : 1), dim3(1024), cs, p, blocks);
 }
