@@ -36,7 +36,8 @@
  *   - A kernel that gives up a bounded internal wait records
  *     RA_ERR_DEVICE_TIMEOUT in a per-device error word; ra_get_device_status
  *     reads (and clears) it.  Kernels never trap.  The word is sticky: while it
- *     is set, every later forward, backward or SWC-step kernel on that device
+ *     is set, every later forward, backward or SWC-step kernel and every attention
+ *     over the 8-bit ring of more than 16 queries on that device
  *     does no work and leaves its outputs unwritten, although its entry point
  *     returned RA_OK when it was enqueued.  Check ra_get_device_status before
  *     trusting outputs produced after a possible timeout; it clears the word.
@@ -336,8 +337,9 @@ ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, cons
  *                      tokens of a slot (the last one of a slot may be shorter) and
  *                      head.  A code stands for code * scale.
  * Scales are powers of two, so that code * scale is a bf16 number; another
- * positive scale is rounded to bf16, as is the product.  The two e4m3 codes of NaN
- * are not used (they read as +-480); a scale of NaN makes its block NaN.
+ * positive scale is rounded to bf16, as is its product with a code of V.  The two
+ * e4m3 codes of NaN are not part of the format (what they read as is not defined);
+ * a scale of NaN makes its block NaN.  Limits: W * s <= 2^30, B * H * W * s <= 2^40.
  *
  * ra_cache8_append -- `frames` new frames (1 .. W), the first being frame number
  *   `frame` >= 0 of the stream, into their slots.  k, v: strided bf16
@@ -355,7 +357,9 @@ ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, cons
  *   key_counts : NULL, or device int32 [B]: batch element b attends to the first
  *                key_counts[b] rows only (clamped to [0, held * s]).
  *   lse        : NULL, or device fp32 [B, H, nq] (natural log).
- *   A query without keys gets O = 0 and lse = -inf.
+ *   A query without keys gets O = 0 and lse = -inf.  P is rounded to bf16 for its
+ *   product with V whatever ra_set_pv_precision says: at 2^-8 of a weight that is
+ *   far below the codes' own rounding, 2^-4 of a value.
  *   workspace  : caller-owned device memory of ra_cache8_attention_workspace_bytes
  *                for the same sizes (0 for some), 16-byte aligned; calls that may
  *                overlap on the GPU need one each.

@@ -70,8 +70,10 @@ def build_binding(force: bool = False) -> str:
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = BINDING + f".tmp{os.getpid()}"
+    # the compiler on PATH, as nvcc's host compiler: one that links its own copy of
+    # libstdc++ into the extension makes two in the process, and printing an error crash
     subprocess.check_call([
-        os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
+        "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", INCLUDE,
         "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
         "-I", sysconfig.get_path("include"), "-I", os.path.join(cuda, "include"), BINDING_SRC, "-o", tmp,
         "-L", os.path.join(torch, "lib"),

@@ -116,4 +116,4 @@ extern "C" ra_status ra_set_wait_timeout_ns(long long timeout_ns)
     return RA_OK;
 }
 
-extern "C" int ra_version(void) { return 1 * 10000 + 0 * 100 + 0; }
+extern "C" int ra_version(void) { return 1 * 10000 + 1 * 100 + 0; }

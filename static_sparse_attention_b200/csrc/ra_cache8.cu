@@ -237,8 +237,10 @@ ra_status check_cache8(const void* k8, const void* v8, const float* k_scale, con
         return fail(RA_ERR_UNSUPPORTED, "head dim %d is not supported (64 or 128)", d);
     if (s < 1 || W < 1)
         return fail(RA_ERR_INVALID_ARG, "s and window_frames must be >= 1");
-    if (static_cast<long long>(s) * W > (1LL << 31) - 1)
+    if (static_cast<long long>(s) * W > CACHE8_MAX_ROWS)
         return fail(RA_ERR_UNSUPPORTED, "window of %lld tokens is too long", static_cast<long long>(s) * W);
+    if (static_cast<long long>(B) * H > (1LL << 40) / (static_cast<long long>(s) * W))
+        return fail(RA_ERR_UNSUPPORTED, "ring too large");
     return RA_OK;
 }
 

@@ -15,6 +15,7 @@
 namespace ra {
 
 constexpr int CACHE8_BLOCK = 64;  // tokens of a frame that share a scale
+constexpr long long CACHE8_MAX_ROWS = 1LL << 30;  // of a head: a few rows further still fit an int
 
 inline int cache8_blocks(int s) { return (s + CACHE8_BLOCK - 1) / CACHE8_BLOCK; }
 

@@ -404,6 +404,8 @@ template <int D>
 __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, long long rows)
 {
     wait_for_previous();
+    if (p.err && *reinterpret_cast<volatile int*>(p.err) != 0)
+        return;  // a block gave up: the parts are not whole
     const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (at >= rows)
@@ -518,12 +520,14 @@ ra_status check_attention(int B, int H, int d, int nq, int s, int W, int held)
         return fail(RA_ERR_UNSUPPORTED, "head dim %d is not supported (64 or 128)", d);
     if (s < 1 || W < 1)
         return fail(RA_ERR_INVALID_ARG, "s and window_frames must be >= 1");
-    if (static_cast<long long>(s) * W > (1LL << 31) - 1 - 128)
+    if (static_cast<long long>(s) * W > CACHE8_MAX_ROWS)
         return fail(RA_ERR_UNSUPPORTED, "window of %lld tokens is too long", static_cast<long long>(s) * W);
     if (held < 0 || held > W)
         return fail(RA_ERR_INVALID_ARG, "frames held must be in [0, window_frames] (%d of %d)", held, W);
     if (nq < 1 || nq > (1 << 24))
         return fail(RA_ERR_INVALID_ARG, "nq must be in [1, 2^24] (%d)", nq);
+    if (static_cast<long long>(B) * H > (1LL << 32) / nq)
+        return fail(RA_ERR_UNSUPPORTED, "tensor too large");
     return RA_OK;
 }
 

@@ -43,8 +43,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
-#include <mutex>
 
 #include "ra_cache8_attention.cuh"
 #include "ra_internal.h"
@@ -629,14 +629,17 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
 template <int D>
 ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
 {
-    static std::once_flag once;
-    static cudaError_t err = cudaSuccess;
-    std::call_once(once, [] {
-        err = cudaFuncSetAttribute(cache8_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   Layout<D>::SMEM);
-    });
-    if (err != cudaSuccess)
-        return cuda_fail(err, "cudaFuncSetAttribute(cache8_tiles_kernel)");
+    // the attribute belongs to the function on one device
+    static std::atomic<unsigned long long> set{0};
+    int dev = 0;
+    RA_CUDA_TRY(cudaGetDevice(&dev));
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev >= 64 || !(set.load(std::memory_order_acquire) & bit)) {
+        RA_CUDA_TRY(cudaFuncSetAttribute(cache8_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Layout<D>::SMEM));
+        if (dev < 64)
+            set.fetch_or(bit, std::memory_order_release);
+    }
     const dim3 grid(static_cast<unsigned>(p.q_tiles) * p.splits, p.H, B);
     cache8_tiles_kernel<D><<<grid, THREADS, Layout<D>::SMEM, cs>>>(p);
     return cuda_fail(cudaGetLastError(), "cache8_tiles_kernel launch");

@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
 {
     constexpr int LPR = D / 8, TOKENS = THREADS / LPR;
     const Rows& t = p.t[blockIdx.y];
-    let_next_launch();
+    if (t.dw_part)  // the sum of the blocks' parts is launched behind this kernel
+        let_next_launch();
     const int sub = threadIdx.x % LPR;
     const int tok = static_cast<int>(threadIdx.x) / LPR;
     const bool norm = t.weight != nullptr;
@@ -237,8 +238,9 @@ ra_status check_strides(const char* what, long long* sb, long long* sn, long lon
     for (int i = 0; i < 3; ++i) {
         if (size[i] == 1)
             *s[i] = 0;  // never used
-        if (*s[i] < 0 || *s[i] % 8 != 0 || *s[i] > (1LL << 46))
-            return fail(RA_ERR_INVALID_ARG, "%s strides must be multiples of 8 elements in [0, 2^46]", what);
+        if (*s[i] < 0 || *s[i] % 8 != 0 || *s[i] > (1LL << 46) / (size[i] > 1 ? size[i] : 1))
+            return fail(RA_ERR_INVALID_ARG,
+                        "%s strides must be multiples of 8 elements, >= 0, and span at most 2^46 elements", what);
     }
     return RA_OK;
 }
@@ -398,6 +400,8 @@ ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, i
         t.H = in[i]->heads;
         H += t.H;
     }
+    if (static_cast<long long>(B) * H * n > (1LL << 40))
+        return fail(RA_ERR_UNSUPPORTED, "tensor too large");
     p->heads = heads_per_chunk(p->tiles, B, H);
     for (int i = 0; i < 2; ++i)
         p->t[i].chunks = (p->t[i].H + p->heads - 1) / p->heads;

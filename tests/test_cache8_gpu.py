@@ -233,6 +233,100 @@ def test_attention_of_a_ragged_batch(nq, d):
     _check(q, ring, s, held, counts, what=f"ragged, nq={nq}")
 
 
+def test_attention_of_whole_frames():
+    """Frames of 1560 tokens, 40 heads: every block walks all 98 steps of keys (its
+    rings turn over many times) and a tile of 24 queries is left; two heads checked."""
+    _gpu.need_gpu()
+    ra = _gpu.ra()
+    B, H, d, s, W = 1, 40, 128, 1560, 5
+    (k8, v8, ks, vs), _ = _ring(B, H, d, s, W, seed=4)
+    q = torch.randn(B, H, s, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).bfloat16()
+    lse = torch.empty(B, H, s, device="cuda")
+    o = ra.cache8_attention(q, k8, v8, ks, vs, 4, lse=lse)
+    assert ra.device_status() == ra.RA_OK
+    for h in (0, 39):
+        at = slice(h, h + 1)
+        want, want_lse, ob, lb = _reference(q[:, at], k8[:, at, :4 * s], v8[:, at, :4 * s], ks[:, at, :4], vs[:, at, :4], s,
+                                            [4 * s], 1 / math.sqrt(d))
+        assert bool(((o[:, at].double().cpu() - want).abs() <= ob).all())
+        assert bool(((lse[:, at].double().cpu() - want_lse).abs() <= lb).all())
+
+
+def test_scales_that_are_no_powers_of_two():
+    """Another quantiser's scales: code * scale rounded to bf16 (of K in the product's
+    order), so a value is off by at most three bf16 roundings."""
+    _gpu.need_gpu()
+    ra = _gpu.ra()
+    B, H, d, s, W = 1, 2, 64, 70, 4
+    (k8, v8, ks, vs), _ = _ring(B, H, d, s, W, seed=8)
+    ks.mul_(1.3)
+    vs.mul_(0.7)
+    for nq in (3, 200):
+        q = torch.randn(B, H, nq, d, device="cuda").bfloat16()
+        o = ra.cache8_attention(q, k8, v8, ks, vs, W)
+        k, v = _values(k8, ks, s), _values(v8, vs, s)
+        x = q.double().cpu() @ k.transpose(2, 3) / math.sqrt(d)
+        p = torch.softmax(x, -1)
+        off = 3 * _heads.BF16
+        e = (q.double().cpu().abs() @ k.abs().transpose(2, 3) / math.sqrt(d)).amax(-1, keepdim=True) * off
+        bound = (p @ v).abs() * _heads.BF16 + (p @ v.abs()) * (off + _heads.BF16 + torch.expm1(2 * e))
+        assert bool(((o.double().cpu() - p @ v).abs() <= bound).all())
+
+
+def test_python_refusals():
+    """Tensors of the wrong type, shape, layout or device are refused before any launch."""
+    _gpu.need_gpu()
+    ra = _gpu.ra()
+    B, H, d, s, W = 2, 2, 64, 10, 3
+    ring, _ = _ring(B, H, d, s, W)
+    k8, v8, ks, vs = ring
+    q = torch.randn(B, H, 4, d, device="cuda").bfloat16()
+    x = torch.randn(B, s, H, d, device="cuda").bfloat16()
+    counts = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(q=q[:1]), dict(q=q.transpose(1, 2)), dict(q=q[..., :32]),
+                dict(k8=k8.view(torch.uint8)), dict(v8=v8[:, :, :-1]), dict(ks=ks.double()), dict(vs=vs[:, :, :2]),
+                dict(ks=ks[:, :, :2]), dict(counts=counts.long()), dict(counts=counts[:1]), dict(counts=counts.cpu()),
+                dict(out=torch.empty(B, H, 4, d, device="cuda")), dict(lse=torch.empty(B, H, 5, device="cuda")),
+                dict(lse=torch.empty(B, H, 4, device="cuda", dtype=torch.bfloat16))):
+        a = dict(q=q, k8=k8, v8=v8, ks=ks, vs=vs, counts=counts, out=None, lse=None)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            ra.cache8_attention(a["q"], a["k8"], a["v8"], a["ks"], a["vs"], W, key_counts=a["counts"], out=a["out"],
+                                lse=a["lse"])
+    for held in (-1, W + 1):
+        with pytest.raises(ra.RaError):
+            ra.cache8_attention(q, *ring, held)
+    with pytest.raises(ra.RaError):
+        ra.cache8_attention(q, *ring, W, out=q)  # aliases its input
+    for k, v in ((x.half(), x), (x[:, :7], x[:, :7]), (x, x[:, :, :1]), (x.cpu(), x), (x.transpose(2, 3), x.transpose(2, 3))):
+        with pytest.raises(ValueError):
+            ra.cache8_append(k, v, *ring, 0)
+    with pytest.raises(ra.RaError):
+        ra.cache8_append(x.repeat(1, W + 1, 1, 1), x.repeat(1, W + 1, 1, 1), *ring, 0)  # two frames in a slot
+    with pytest.raises(ValueError):
+        ra.cache8_append(x, x, *ring, 0, k_weight=torch.ones(d + 1, device="cuda"))
+    with pytest.raises(ra.RaError):
+        ra.cache8_append(x, x, *ring, 0, rope=ra.rope3d(4, 3, 3, d))  # frames of 9 tokens
+    with pytest.raises(ra.RaError):
+        ra.cache8_append(x, x, *ring, 4, rope=ra.rope3d(4, 2, 5, d))  # frame 4 of 4
+    w = torch.ones(d, device="cuda")
+    for bad in (dict(q=x.float()), dict(q=x.cpu()), dict(q=x[0]), dict(k=x[:, :3]), dict(qw=w[:8]), dict(qw=w.half()),
+                dict(k=None, kw=w), dict(rope=(w, w)), dict(rope=(w, w, w)), dict(q_out=torch.empty_like(x))):
+        a = dict(q=x, k=x, qw=w, kw=None, rope=ra.rope3d(1, 2, 5, d), q_out=None)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            ra.qk_norm_rope(a["q"], a["k"], a["qw"], a["kw"], rope=a["rope"], q_out=a["q_out"])
+    dy = torch.empty(B, H, s, d, device="cuda", dtype=torch.bfloat16)
+    for args in ((x, x, dy, None), (x, None, dy, dy), (x, None, x, None)):
+        with pytest.raises(ValueError):
+            ra.qk_norm_rope_bwd(*args, w)
+    with pytest.raises(ValueError):
+        ra.qk_norm_rope_bwd(x, None, dy, None, w, workspace=torch.empty(8, device="cuda"))
+    with pytest.raises(ValueError):
+        ra.qk_norm_rope_bwd(x, None, dy, None, None, rope=ra.rope3d(1, 2, 5, d), dq_weight=w)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("nq", [1, 200])
 def test_attention_without_frames(nq):
     _gpu.need_gpu()

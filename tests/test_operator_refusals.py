@@ -44,6 +44,11 @@ def test_norm_rope_refuses(ra, kw):
     assert ra.ra_last_error()
 
 
+def test_norm_rope_refuses_what_is_too_large(ra):
+    assert _fwd(ra, q=_rows(ra, 10 * MB, heads=60000, stride_h=0), B=60000, n=1000) == ra.RA_ERR_UNSUPPORTED
+    assert _fwd(ra, q=_rows(ra, 10 * MB, stride_n=1 << 44)) == ra.RA_ERR_INVALID_ARG
+
+
 def test_norm_rope_refuses_head_dims(ra):
     assert _fwd(ra, d=96) == ra.RA_ERR_UNSUPPORTED
     assert _fwd(ra, d=256) == ra.RA_ERR_UNSUPPORTED
@@ -182,7 +187,8 @@ def _attend(ra, Q=10 * MB, k8=30 * MB, v8=31 * MB, ks=32 * MB, vs=33 * MB, O=40 
     (dict(d=32), 2), (dict(nq=0), 1), (dict(nq=1 << 25), 1), (dict(held=5), 1), (dict(held=-1), 1), (dict(s=0), 1),
     (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(counts=60 * MB + 2), 1), (dict(lse=61 * MB + 1), 1),
     (dict(O=10 * MB), 1), (dict(O=30 * MB), 1), (dict(lse=32 * MB), 1), (dict(lse=40 * MB), 1), (dict(counts=40 * MB), 1),
-    (dict(s=1 << 20, W=1 << 12), 2),
+    (dict(s=1 << 20, W=1 << 12), 2), (dict(s=1 << 20, W=1 << 10, H=60000, B=60000), 2),
+    (dict(H=60000, B=60000, nq=1000), 2),
 ])
 def test_cache8_attention_refuses(ra, kw, status):
     assert _attend(ra, **kw) == status
@@ -198,6 +204,22 @@ def test_cache8_attention_refuses_workspaces(ra):
         assert _attend(ra, **long, **kw) == ra.RA_ERR_INVALID_ARG
         assert ra.ra_last_error()
     assert ra.ra_cache8_attention_workspace_bytes(2, 1, 128, 3, 20, 4, 3, None) == ra.RA_ERR_INVALID_ARG
+
+
+def test_binding_shares_the_process_standard_library(ra):
+    """The extension uses the process's libstdc++ (a copy of its own crashed when an
+    error's numbers were printed on a machine with a GPU), and a wrong call says so."""
+    import os
+    import subprocess
+    binding = ra._load_binding()
+    path = os.path.join(os.path.dirname(ra.LIB_PATH), "_torch_binding.so")
+    assert os.path.samefile(binding.__file__, path)
+    needed = subprocess.run(["readelf", "-d", path], capture_output=True, text=True, check=True).stdout
+    assert "libstdc++.so" in needed
+    with pytest.raises(TypeError, match="10 arguments, got 1"):
+        binding.qk_norm_rope(None)
+    with pytest.raises(ValueError, match="q must be a tensor"):
+        ra.qk_norm_rope(None)
 
 
 def test_swc_cache8_refuses(ra):
