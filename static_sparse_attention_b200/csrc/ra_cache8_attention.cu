@@ -98,7 +98,7 @@ struct Group {
 struct Places {
     const uint8_t* k;     // row r
     const uint8_t* v;     // row 2 c
-    const uint8_t* ahead; // of K (lanes 0-15) or V: row lane % 16, for the prefetch
+    const uint8_t* ahead; // row lane % 16 of K (lanes 0-15) or V, for the prefetch
     const float* scale;   // of K or V
 };
 
@@ -146,8 +146,19 @@ __device__ __forceinline__ void load_codes(Group<D>& g, const Places& at, int ke
     }
 }
 
-// The group that starts at key0: its codes (zeros behind `end`) and scales; and ask
-// L2 for the rows of one PREFETCH rounds later, one of K or V a lane.
+// Ask L2 for a later group's codes and scales: one row of K or V a lane.
+template <int D>
+__device__ __forceinline__ void prefetch_group(const AttnParams& p, const Places& at, long long bh, int key0, int end)
+{
+    const int key = key0 + static_cast<int>(threadIdx.x & 15);
+    if (key < end) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at.ahead + static_cast<long long>(key0) * D));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at.scale + scale_index(p, bh, key)));
+    }
+}
+
+// The group that starts at key0: its codes (zeros behind `end`) and scales; and the
+// prefetch of one PREFETCH rounds later.
 template <int D>
 __device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, const Places& at, long long bh, int key0,
                                            int end)
@@ -158,9 +169,7 @@ __device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, con
         load_codes<D, false>(g, at, key0, end);
     const int key = key0 + static_cast<int>(threadIdx.x & 15);
     g.scale = key < end ? at.scale[scale_index(p, bh, key)] : 0.f;
-    const int later = key0 + PREFETCH * WARPS * GROUP;
-    if (later + GROUP <= end)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at.ahead + static_cast<long long>(later) * D));
+    prefetch_group<D>(p, at, bh, key0 + PREFETCH * WARPS * GROUP, end);
 }
 
 // The running state of 8 NT queries in one warp: a lane holds queries 8 t + 2 c and
@@ -298,6 +307,9 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kerne
     int key = begin + warp * GROUP;
     if (key < end)
         load_group(even, p, at, bh, key, end);
+#pragma unroll
+    for (int i = 1; i < PREFETCH; ++i)
+        prefetch_group<D>(p, at, bh, key + i * WARPS * GROUP, end);
 
     State<D, NT> st;
 #pragma unroll

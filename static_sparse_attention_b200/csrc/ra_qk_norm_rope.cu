@@ -13,8 +13,7 @@
 //
 // A row is held by d / 8 lanes, 16 bytes each (ra_head_rows.cuh).  A lane stays
 // with its token and walks heads, so the cosines and sines of a token are
-// loaded once for up to HEADS_MAX heads; rows are fetched HEADS_IN_FLIGHT at a
-// time.
+// loaded once for many rows, which are fetched HEADS_IN_FLIGHT at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -28,14 +27,13 @@ namespace ra {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int HEADS_MAX = 8;        // heads that a lane walks for one token
 constexpr int HEADS_IN_FLIGHT = 4;  // rows loaded before the first is used
 // The backward keeps 24 warps an SM: at 16 (122 registers a thread, nothing asked of
 // the compiler) 63960 tokens of 40 heads of 128 take 778 us, at 24 (85 registers)
 // 690, at 32 (64 registers, spills) 830.
 constexpr int BWD_BLOCKS_PER_SM = 3;
 constexpr int BWD_BLOCKS = 148 * BWD_BLOCKS_PER_SM;  // and as many partial sums of a weight's gradient
-constexpr int FWD_WANT_BLOCKS = 148 * 4;
+constexpr int FWD_SLOTS = 148 * 5;
 
 // One of the two tensors (q or k) of a call.
 struct Rows {
@@ -362,17 +360,32 @@ ra_status check_sizes(int B, int n, int d, float eps)
     return RA_OK;
 }
 
-// Heads that a lane walks: as many as leave every SM its blocks.
-int heads_per_chunk(long long tiles, int B, int H)
+// Heads that a lane walks for one token: all of them when there are tokens enough (a
+// token's rows are then read in one stretch: 63960 tokens of 40 heads of 128 backward
+// 704 us against 758 with 8 heads at a time), else as many as cost least, in rounds
+// of the `slots` blocks that run at once (whole rounds where the blocks stay and take
+// several items each) times the batches of loads that a lane waits for, with a
+// quarter of one for the look-up of its angles.
+int heads_per_chunk(long long tiles, int B, int H, int slots, bool whole_rounds)
 {
-    int heads = HEADS_MAX;
-    while (heads > 1 && tiles * B * ((H + heads - 1) / heads) < FWD_WANT_BLOCKS)
-        heads /= 2;
-    return heads;
+    int best = H;
+    double least = 0;
+    for (int c = 1; c <= H && c <= 64; ++c) {
+        const int heads = (H + c - 1) / c;
+        const long long blocks = tiles * B * ((H + heads - 1) / heads);
+        double rounds = static_cast<double>(blocks) / slots;
+        rounds = whole_rounds ? std::ceil(rounds) : (rounds > 1 ? rounds : 1);
+        const double cost = rounds * ((heads + HEADS_IN_FLIGHT - 1) / HEADS_IN_FLIGHT + 0.25);
+        if (c == 1 || cost < least) {
+            least = cost;
+            best = heads;
+        }
+    }
+    return best;
 }
 
 ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, int n, int d, const ra_rope* rope,
-               int frame0, float eps)
+               int frame0, float eps, int slots, bool whole_rounds)
 {
     std::memset(p, 0, sizeof *p);
     ra_status st = rope_args(rope, frame0, n, d, &p->rope);
@@ -398,11 +411,11 @@ ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, i
         t.weight = in[i]->weight;
         t.weight_fp32 = in[i]->weight_fp32;
         t.H = in[i]->heads;
-        H += t.H;
+        H = t.H > H ? t.H : H;
     }
     if (static_cast<long long>(B) * H * n > (1LL << 40))
         return fail(RA_ERR_UNSUPPORTED, "tensor too large");
-    p->heads = heads_per_chunk(p->tiles, B, H);
+    p->heads = heads_per_chunk(p->tiles, B, H, slots, whole_rounds);
     for (int i = 0; i < 2; ++i)
         p->t[i].chunks = (p->t[i].H + p->heads - 1) / p->heads;
     return RA_OK;
@@ -442,7 +455,7 @@ extern "C" ra_status ra_qk_norm_rope(const ra_head_rows* q, const ra_head_rows* 
     if (st != RA_OK)
         return st;
     Params p;
-    if ((st = fill(&p, q, k, B, n, d, rope, frame0, eps)) != RA_OK)
+    if ((st = fill(&p, q, k, B, n, d, rope, frame0, eps, k ? FWD_SLOTS / 2 : FWD_SLOTS, false)) != RA_OK)
         return st;
     if (n == 0)
         return RA_OK;
@@ -485,7 +498,7 @@ extern "C" ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_ro
     if (st != RA_OK)
         return st;
     Params p;
-    if ((st = fill(&p, q, k, B, n, d, rope, frame0, eps)) != RA_OK)
+    if ((st = fill(&p, q, k, B, n, d, rope, frame0, eps, BWD_BLOCKS, true)) != RA_OK)
         return st;
     const ra_head_grads* grads[2] = {dq, k ? dk : nullptr};
     const char* name[2] = {"dq", "dk"};
