@@ -31,8 +31,9 @@ namespace {
 
 constexpr int PASSES = 4;         // row groups of a block held in registers
 constexpr int ROWS_PER_PASS = 16; // so that PASSES * ROWS_PER_PASS rows make a block
-constexpr int HEADS_MAX = 8;
-constexpr int WANT_BLOCKS = 148 * 4;
+constexpr int HEADS_MAX = 24;  // of a thread block (12 frames of 3555 tokens: 157 us, with 8 heads 162)
+constexpr int SLOTS = 148 * 3;
+constexpr double START = 1.5;
 static_assert(PASSES * ROWS_PER_PASS == CACHE8_BLOCK, "a block of tokens is held whole");
 
 struct AppendParams {
@@ -222,6 +223,27 @@ __global__ void __launch_bounds__(ROWS_PER_PASS * D / 8, 3 * 128 / D) cache8_app
 
 }  // namespace
 
+namespace {
+
+// Heads of a thread block: least rounds of the SLOTS blocks that run at once times
+// the heads of one and START more for its start; at most HEADS_MAX.
+int heads_per_block(long long units, int H)
+{
+    int best = 1;
+    double least = 0;
+    for (int heads = 1; heads <= H && heads <= HEADS_MAX; ++heads) {
+        const double rounds = static_cast<double>(units * ((H + heads - 1) / heads)) / SLOTS;
+        const double cost = (rounds > 1 ? rounds : 1) * (heads + START);
+        if (heads == 1 || cost < least) {
+            least = cost;
+            best = heads;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
 ra_status check_cache8(const void* k8, const void* v8, const float* k_scale, const float* v_scale, int B, int H, int d,
                        int s, int W)
 {
@@ -311,11 +333,8 @@ extern "C" ra_status ra_cache8_append(const ra_head_rows* k, const ra_head_rows*
             if (overlap(out[i], out[j]))
                 return fail(RA_ERR_INVALID_ARG, "the rings and scales may not alias one another");
     }
-    // heads of a thread block: up to HEADS_MAX, fewer while that leaves SMs without work
     const long long units = static_cast<long long>(frames) * p.blocks;
-    p.heads = HEADS_MAX;
-    while (p.heads > 1 && units * B * 2 * ((H + p.heads - 1) / p.heads) < WANT_BLOCKS)
-        p.heads /= 2;
+    p.heads = heads_per_block(units * B * 2, H);
     p.groups = (H + p.heads - 1) / p.heads;
     const long long blocks = units * p.groups;
     if (blocks > (1LL << 31) - 1)
