@@ -3,12 +3,12 @@
 //     O = softmax(scale * Q K^T) V over the first count keys of each head.
 //
 // Few-query kernel: one block per (head, 8 or 16 queries, range of keys), four
-// warps that take groups of 16 keys in turn, the next group on its way while one is
-// computed.  Both products are 16 x 8 x 16 warp products with fp32 sums that keep the
-// queries as columns: S^T = K Q^T and O^T += V^T P^T, so that eight queries (or one)
-// take half the registers that they would as rows.  The order of channels and keys
-// inside a product is free and chosen by what a lane loads: 16 contiguous bytes of a
-// key's row, and of a value's row.
+// warps that take groups of 16 keys in turn; L2 is asked for them some rounds ahead.
+// Both products are 16 x 8 x 16 warp products with fp32 sums that keep the queries as
+// columns: S^T = K Q^T and O^T += V^T P^T, so that eight queries (or one) take half
+// the registers that they would as rows.  The order of channels and keys inside a
+// product is free and chosen by what a lane loads: 16 contiguous bytes of a key's
+// row, and of a value's row.
 //   S^T: the codes go to fp16 as they are (one instruction for two), Q is brought to
 //        fp16 by a power of two for each query, and the key's scale multiplies the
 //        score.
@@ -282,8 +282,13 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
     }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kernel(const AttnParams p)
+// AHEAD: a second group is on its way in registers while one is computed; else the
+// next one is loaded behind it (L2 has been asked for it), and more warps fit.  Blocks
+// an SM of either (128 and 64 channels):
+__host__ __device__ constexpr int rows_blocks(int D, int NT, bool ahead) { return NT > 1 ? 2 : ahead ? 3 : D == 64 ? 5 : 4; }
+
+template <int D, int NT, bool AHEAD>
+__global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_rows_kernel(const AttnParams p)
 {
     constexpr int ROWS = COLS * NT;
     __shared__ float sm_o[WARPS][ROWS][D + 4];
@@ -301,7 +306,7 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kerne
     if (p.splits > 1)
         let_next_launch();
 
-    // two groups in registers, taken in turn: one on its way while the other is computed
+    // AHEAD: two groups, taken in turn
     Group<D> even, odd;
     const Places at = places_of<D>(p, bh);
     int key = begin + warp * GROUP;
@@ -353,18 +358,25 @@ __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 3 : 2) cache8_rows_kerne
     }
 
     auto step = [&](const Group<D>& now, Group<D>& next) {
-        if (key + WARPS * GROUP < end)
-            load_group(next, p, at, bh, key + WARPS * GROUP, end);
+        const int ahead = key + WARPS * GROUP;
+        if (AHEAD && ahead < end)
+            load_group(next, p, at, bh, ahead, end);
         if (__any_sync(0xFFFFFFFFu, lane >= 16 && !(now.scale <= 128.f)))
             group_step<D, NT, true>(st, now, key, end);
         else
             group_step<D, NT, false>(st, now, key, end);
-        key += WARPS * GROUP;
+        if (!AHEAD && ahead < end)
+            load_group(next, p, at, bh, ahead, end);
+        key = ahead;
     };
     while (key < end) {
-        step(even, odd);
-        if (key < end)
-            step(odd, even);
+        if (!AHEAD) {
+            step(even, even);
+        } else {
+            step(even, odd);
+            if (key < end)
+                step(odd, even);
+        }
     }
 #pragma unroll
     for (int t = 0; t < NT; ++t)
@@ -627,15 +639,18 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
             return st;
     } else {
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
-        const bool one = nq <= COLS;
-        if (d == 64 && one)
-            cache8_rows_kernel<64, 1><<<grid, WARPS * 32, 0, cs>>>(p);
-        else if (d == 64)
-            cache8_rows_kernel<64, 2><<<grid, WARPS * 32, 0, cs>>>(p);
-        else if (one)
-            cache8_rows_kernel<128, 1><<<grid, WARPS * 32, 0, cs>>>(p);
-        else
-            cache8_rows_kernel<128, 2><<<grid, WARPS * 32, 0, cs>>>(p);
+        // One wave of blocks waits for its loads: the second group hides them (12480
+        // keys, 24 heads of 128: 25 us, without it 27-29).  Several waves want more
+        // warps (eight caches of up to 32768 keys: 179 us, with it 189).  Sixteen queries
+        // need the registers for two groups either way (250 us; one group and 12 warps 273).
+        const bool one = nq <= COLS, ahead = static_cast<long long>(grid.x) * H * B <= 2 * ONE_WAVE;
+        auto kernel = d == 64 ? (!one ? cache8_rows_kernel<64, 2, true>
+                                 : ahead ? cache8_rows_kernel<64, 1, true>
+                                         : cache8_rows_kernel<64, 1, false>)
+                              : (!one ? cache8_rows_kernel<128, 2, true>
+                                 : ahead ? cache8_rows_kernel<128, 1, true>
+                                         : cache8_rows_kernel<128, 1, false>);
+        kernel<<<grid, WARPS * 32, 0, cs>>>(p);
         RA_CUDA_TRY(cudaGetLastError());
     }
     if (pl.splits == 1)
