@@ -15,7 +15,10 @@
 //   P V: the values go to bf16 code * scale (ra_cache8.cuh) and P to bf16, whose
 //        range no mixture of scales leaves.
 // Ranges of keys leave partial (maximum, sum, O) to a second kernel that joins them.
-// Bound by memory for few queries (one byte a value of K and V).
+// Bound by memory for few queries (one byte a value of K and V): one query on each of
+// eight caches of 4096 to 32768 keys, 24 heads of 128, 179 us = 5.2 TB/s, 80 % of the
+// measured copy rate (DRAM traffic 0.938 GB of 0.934); the integer pipe, which turns
+// the codes of V to bf16, is 57 % busy.  One launch of a few hundred keys: 7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -487,7 +490,7 @@ constexpr int WANT_BLOCKS = SMS * 16;
 // the few-query kernel takes them in one go with blocks to spare (256 keys, 24 heads
 // of 64, 128 queries: 9.5 against 10.4 us; twice the blocks: 14.5 against 20.7).
 constexpr int FEW_BLOCKS = 192;
-constexpr double STEP_US = 0.9;        // a step of 64 keys of 256 queries
+constexpr double STEP_US = 1.0;        // a step of 64 keys of 256 queries: 0.76 us with 64 channels, 1.1 with 128
 constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
 constexpr double JOIN_BYTES_PER_US = 5e6;
 

@@ -2,24 +2,32 @@
 // on the tensor cores (tcgen05, accumulators in TMEM).
 //
 // One CTA per (head, 256 queries, range of keys), one CTA per SM, keys in steps
-// of 64.  Four warpgroups in fixed roles:
+// of 64.  Five warpgroups in fixed roles:
 //   warps 0-3, 4-7  softmax of query tile 0 and 1 (128 rows each): thread t of the
 //                   group owns row t (TMEM lane t); per step reads S, keeps the
 //                   running maximum and sum, writes P (bf16) back over S; at the end
 //                   the epilogue.
-//   warp 14         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
+//   warp 18         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
 //                   are contiguous) into a ring of shared memory, RAW steps ahead; its
 //                   lanes turn the rows' scales into the factors of the conversion.
-//   warps 8-11      convert: codes become code * scale in bf16 -- exactly, see
+//                   (Warp 19 makes up the warpgroup.)
+//   warps 8-15      convert: codes become code * scale in bf16 -- exactly, see
 //                   ra_cache8.cuh -- in the MMA's 128-byte swizzle, in a ring of K
 //                   stages and one of V stages.
-//   warps 12, 13    MMA of tile 0 and 1 (12 allocates TMEM): one elected lane issues
+//   warps 16, 17    MMA of tile 0 and 1 (16 allocates TMEM): one elected lane issues
 //                   S_h = Q K_h^T (N = 64) into S buffer h % 2 and O += P_h V_h, in
 //                   the order S_0, S_1, PV_0, S_2, PV_1, S_3, ...
-// Two query tiles share one conversion: per step it costs about 5.5 integer and
-// multiply instructions for two codes, 1400 warp instructions for 64 keys of 128
-// channels, against 2900 for the softmax of 2 x 128 x 64 scores and 1280 clocks of
-// the tensor pipe; with one tile a CTA it would not hide behind them.
+// Two query tiles share one conversion: 4.5 integer and multiply instructions for two
+// codes, 1400 warp instructions for a step of 64 keys of 128 channels, beside 2900 for
+// the softmax of 2 x 128 x 64 scores and 1280 clocks of the tensor pipe.
+//
+// Measured: 1560 queries, 24960 keys, 40 heads of 128 (280 CTAs, two rounds of SMs)
+// 827 us = 964 TFLOP/s, 59 % of the measured bf16 burst; 2000 clocks a step, issue
+// slots 67 %, exp2 and tensor pipes half busy each.  What a step waits for is the
+// softmax warps' own chain (1500 clocks of exponentials with the convert warps beside
+// them, 400 of barriers and TMEM).  On the way: one MMA warp for both tiles 1134 us (its
+// waits, 100-200 clocks each, stood between one tile's products and the other's), four
+// convert warps 918.
 //
 // A word of four codes is turned into two pairs, channels (0, 2) and (1, 3), which
 // saves the byte permutes.  So channels lie in the order 0, 2, 1, 3 within every
@@ -37,9 +45,8 @@
 // through the async proxy: the proxy fence between the two stands in the MMA warp,
 // behind its wait for the writers' barrier.
 //
-// With the codes fetched by the convert warps' own loads, two steps ahead, a step
-// took 2350 clocks (1.11 ms for 1560 queries, 24960 keys, 40 heads of 128): they
-// waited for their loads.
+// (With the codes fetched by the convert warps' own loads, two steps ahead, these
+// waited for their loads.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -57,7 +64,7 @@ constexpr int STEP = 64;           // keys of a step
 constexpr int TILE_ROWS = 128;     // queries of a tile
 constexpr int THREADS = 640;
 constexpr int CONVERT_WARP = 8, MMA_WARP = 16, FETCH_WARP = 18;  // MMA: 16 and 17, one for each tile
-// Registers a thread of each warpgroup keeps of the 128 that the block is launched
+// Registers a thread of each warpgroup keeps of the 96 that the block is launched
 // with: the softmax holds 64 scores, P and its sums.
 constexpr int SOFTMAX_REGS = 152, CONVERT_REGS = 56, MMA_REGS = 64;
 static_assert(2 * SOFTMAX_REGS + 2 * CONVERT_REGS + MMA_REGS <= 5 * 96, "the split draws on the block's own registers");
