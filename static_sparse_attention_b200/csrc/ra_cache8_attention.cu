@@ -490,7 +490,7 @@ constexpr int WANT_BLOCKS = SMS * 16;
 // the few-query kernel takes them in one go with blocks to spare (256 keys, 24 heads
 // of 64, 128 queries: 9.5 against 10.4 us; twice the blocks: 14.5 against 20.7).
 constexpr int FEW_BLOCKS = 192;
-constexpr double STEP_US = 1.0;        // a step of 64 keys of 256 queries: 0.76 us with 64 channels, 1.1 with 128
+constexpr double STEP_US = 1.0;        // a step of 64 keys: 0.8 us with 64 channels, 1.1 with 128 (one tile: 0.5, 0.8)
 constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
 constexpr double JOIN_BYTES_PER_US = 5e6;
 

@@ -7,10 +7,10 @@
 //                   group owns row t (TMEM lane t); per step reads S, keeps the
 //                   running maximum and sum, writes P (bf16) back over S; at the end
 //                   the epilogue.
-//   warp 18         fetch: bulk copies of a step's codes (its 64 rows of K, and of V,
-//                   are contiguous) into a ring of shared memory, RAW steps ahead; its
-//                   lanes turn the rows' scales into the factors of the conversion.
-//                   (Warp 19 makes up the warpgroup.)
+//   warps 18, 19    fetch, a step each in turn: bulk copies of a step's codes (its 64
+//                   rows of K, and of V, are contiguous) into a ring of shared memory,
+//                   RAW steps ahead; the lanes turn the rows' scales into the factors
+//                   of the conversion.
 //   warps 8-15      convert: codes become code * scale in bf16 -- exactly, see
 //                   ra_cache8.cuh -- in the MMA's 128-byte swizzle, in a ring of K
 //                   stages and one of V stages.
@@ -28,6 +28,14 @@
 // them, 400 of barriers and TMEM).  On the way: one MMA warp for both tiles 1134 us (its
 // waits, 100-200 clocks each, stood between one tile's products and the other's), four
 // convert warps 918.
+//
+// Up to 128 queries are one tile (ONE).  Its steps are taken in turn by the two
+// softmax groups and MMA warps, each with its own maximum, sum and O, which group 0
+// joins to its own at the end.  With one group at work and one fetch warp a step took
+// 1700 clocks; turns alone changed nothing, a fetch warp's own chain (waits, indexes,
+// factors) being as long.  With both, a step is 1000 clocks at 64 channels (issue
+// slots 67 %) and 1500 at 128, where the conversion is the longest (without it 1150).
+// 32 queries, 12480 keys: 80 heads of 64 113 -> 86 us, 192 heads of 128 269 -> 244.
 //
 // A word of four codes is turned into two pairs, channels (0, 2) and (1, 3), which
 // saves the byte permutes.  So channels lie in the order 0, 2, 1, 3 within every
@@ -63,7 +71,7 @@ namespace {
 constexpr int STEP = 64;           // keys of a step
 constexpr int TILE_ROWS = 128;     // queries of a tile
 constexpr int THREADS = 640;
-constexpr int CONVERT_WARP = 8, MMA_WARP = 16, FETCH_WARP = 18;  // MMA: 16 and 17, one for each tile
+constexpr int CONVERT_WARP = 8, MMA_WARP = 16, FETCH_WARP = 18;  // two warps each of MMA and fetch
 // Registers a thread of each warpgroup keeps of the 96 that the block is launched
 // with: the softmax holds 64 scores, P and its sums.
 constexpr int SOFTMAX_REGS = 152, CONVERT_REGS = 56, MMA_REGS = 64;
@@ -82,38 +90,39 @@ enum : int {
     SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN
 };
 
-template <int D>
+// ONE: a single tile of queries (see Turns).
+template <int D, bool ONE>
 struct Layout {
     static constexpr int CHUNKS = D / 64;                       // 128-byte swizzle atoms across d
     static constexpr int Q_CHUNK = TILE_ROWS * 128;             // bytes of 128 rows x 64 channels
     static constexpr int Q_TILE = CHUNKS * Q_CHUNK;
     static constexpr int KV_CHUNK = STEP * 128;
     static constexpr int KV_TILE = CHUNKS * KV_CHUNK;           // K or V of a step
-    static constexpr int STAGES = 3;                            // of K, and of V
+    static constexpr int STAGES = ONE ? 4 : 3;                  // of K, and of V
     static constexpr int RAW = 4;                               // steps of codes
     static constexpr int RAW_TILE = STEP * D;                   // bytes of K's or V's codes of a step
-    static constexpr int K_OFF = 2 * Q_TILE;
+    static constexpr int K_OFF = (ONE ? 1 : 2) * Q_TILE;
     static constexpr int V_OFF = K_OFF + STAGES * KV_TILE;
     static constexpr int RAW_OFF = V_OFF + STAGES * KV_TILE;    // [RAW][K, V]
     static constexpr int FACTOR_OFF = RAW_OFF + RAW * 2 * RAW_TILE;
     static constexpr int FACTORS = 2 * STEP + 4;                // words: of K's rows, of V's rows, the TWO flag
     static constexpr int BAR_OFF = FACTOR_OFF + RAW * FACTORS * 4;
-    static constexpr int SMEM = BAR_OFF + 272;
+    static constexpr int SMEM = BAR_OFF + 304;                  // barriers, the TMEM address, the abort flag
     static_assert(SMEM <= 227 * 1024, "one block's shared memory");
 };
 
 enum : int {
-    B_K_FULL = 0,      // + stage
-    B_V_FULL = 3,      // + stage
-    B_K_EMPTY = 6,     // + stage
-    B_V_EMPTY = 9,     // + stage
-    B_RAW_FULL = 12,   // + raw stage
-    B_RAW_EMPTY = 16,  // + raw stage
-    B_S_FULL = 20,     // + 2 * tile + buffer
-    B_P_FULL = 24,     // + 2 * tile + buffer
-    B_PV_DONE = 28,    // + tile
-    B_O_FINAL = 30,    // + tile
-    B_COUNT = 32
+    B_K_FULL = 0,      // + stage (up to 4)
+    B_V_FULL = 4,      // + stage
+    B_K_EMPTY = 8,     // + stage
+    B_V_EMPTY = 12,    // + stage
+    B_RAW_FULL = 16,   // + raw stage
+    B_RAW_EMPTY = 20,  // + raw stage
+    B_S_FULL = 24,     // + 2 * tile + buffer
+    B_P_FULL = 28,     // + 2 * tile + buffer
+    B_PV_DONE = 32,    // + tile
+    B_O_FINAL = 34,    // + tile
+    B_COUNT = 36
 };
 constexpr int CONVERT_WARPS = 8;
 
@@ -191,19 +200,30 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t factor, uint32_t& x,
     y = mul_bf16x2(e4m3x2_small(w), factor);
 }
 
-// How the convert threads share a step's rows: 16 codes a thread, rows `row` and
-// every ROW_STEP behind it.
+// What a convert thread takes of a step's K or V: 16 codes of row `row` and of every
+// ROW_STEP-th behind it, and the rows' factors.
 template <int D>
 struct Codes {
     static constexpr int PER_ROW = D / 16;  // threads a row
     static constexpr int ROW_STEP = CONVERT_WARPS * 32 / PER_ROW;
     static constexpr int N = STEP / ROW_STEP;
+    uint4 x[N];
+    uint32_t f[N];
 };
 
-// Convert a step's codes of K or V into a stage.  TWO: some scale of the step needs
-// its second factor.
+template <int D>
+__device__ __forceinline__ void load_codes(Codes<D>& c, const uint8_t* raw, const uint32_t* factors, int row, int part)
+{
+#pragma unroll
+    for (int i = 0; i < Codes<D>::N; ++i) {
+        c.x[i] = *reinterpret_cast<const uint4*>(raw + (row + i * Codes<D>::ROW_STEP) * D + part * 16);
+        c.f[i] = factors[row + i * Codes<D>::ROW_STEP];
+    }
+}
+
+// Convert them into a stage.  TWO: some scale of the step needs its second factor.
 template <int D, bool TWO>
-__device__ __forceinline__ void convert(const uint8_t* raw, const uint32_t* factors, uint8_t* stage, int row, int part)
+__device__ __forceinline__ void store_codes(const Codes<D>& c, uint8_t* stage, int row, int part)
 {
     using C = Codes<D>;
     // 16-byte units 2 part and 2 part + 1 of the row.  With eight threads a row the
@@ -211,21 +231,19 @@ __device__ __forceinline__ void convert(const uint8_t* raw, const uint32_t* fact
     // on different banks.  row and row + i * ROW_STEP have the same swizzle.
     static_assert(C::ROW_STEP % 8 == 0, "one swizzle for all rows of a thread");
     const int swap = D == 128 ? part >> 2 : 0;
-    uint8_t* base = stage + (part >> 2) * Layout<D>::KV_CHUNK + row * 128;
+    uint8_t* base = stage + (part >> 2) * (STEP * 128) + row * 128;
     uint8_t* at0 = base + (((2 * (part & 3) + swap) ^ (row & 7)) << 4);
     uint8_t* at1 = base + (((2 * (part & 3) + 1 - swap) ^ (row & 7)) << 4);
-#pragma unroll 2
+#pragma unroll
     for (int i = 0; i < C::N; ++i) {
-        const uint4 xi = *reinterpret_cast<const uint4*>(raw + (row + i * C::ROW_STEP) * D + part * 16);
-        const uint32_t mi = factors[row + i * C::ROW_STEP];
-        const uint32_t f = __byte_perm(mi, 0, 0x1010);
-        const uint32_t w[4] = {xi.x, xi.y, xi.z, xi.w};
+        const uint32_t f = __byte_perm(c.f[i], 0, 0x1010);
+        const uint32_t w[4] = {c.x[i].x, c.x[i].y, c.x[i].z, c.x[i].w};
         uint32_t out[8];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             codes4(w[j], f, out[2 * j], out[2 * j + 1]);
         if (TWO) {
-            const uint32_t f2 = __byte_perm(mi, 0, 0x3232);
+            const uint32_t f2 = __byte_perm(c.f[i], 0, 0x3232);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 out[j] = mul_bf16x2(out[j], f2);
@@ -234,6 +252,18 @@ __device__ __forceinline__ void convert(const uint8_t* raw, const uint32_t* fact
         *reinterpret_cast<uint4*>(at0 + i * C::ROW_STEP * 128) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(at1 + i * C::ROW_STEP * 128) = swap ? lo : hi;
     }
+}
+
+// The steps of the key range that tile t's softmax group and MMA warp take: all; or,
+// with one tile of queries (ONE), every second one, so that both groups have work.
+struct Turns {
+    int first, stride, n;
+    __device__ __forceinline__ int step(int i) const { return first + i * stride; }
+};
+template <bool ONE>
+__device__ __forceinline__ Turns turns_of(int t, int n)
+{
+    return ONE ? Turns{t, 2, (n - t + 1) / 2} : Turns{0, 1, n};
 }
 
 template <int REGS>
@@ -247,10 +277,10 @@ __device__ __forceinline__ void take_registers()
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-template <int D>
+template <int D, bool ONE>
 __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnParams p)
 {
-    using L = Layout<D>;
+    using L = Layout<D, ONE>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     const uint32_t bars = sbase + L::BAR_OFF;
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         return;  // the join does not read this split
     const int end = min(begin + p.chunk, count);
     const int q0 = q_tile * 2 * TILE_ROWS;
-    const int tiles = p.nq - q0 > TILE_ROWS ? 2 : 1;
+    const int tiles = !ONE && p.nq - q0 > TILE_ROWS ? 2 : 1;
     WaitCtl wc{abort_flag, p.err, p.timeout_ns};
     if (p.splits > 1)
         let_next_launch();
@@ -317,74 +347,88 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     if (warp >= MMA_WARP) {
         // ----------------------------------------------------------------- MMA
         shed_registers<MMA_REGS>();
-        if (warp < FETCH_WARP && warp - MMA_WARP < tiles && n > 0) {
-            const int t = warp - MMA_WARP;
+        const int t = warp - MMA_WARP;
+        const Turns turns = turns_of<ONE>(t, n);
+        if (warp < FETCH_WARP && (ONE || t < tiles) && turns.n > 0) {
             const bool leader = elect_one();
             constexpr uint32_t idesc_s = idesc_bf16_f32(TILE_ROWS, STEP, 0, 0);
             constexpr uint32_t idesc_pv = idesc_bf16_f32(TILE_ROWS, D, 0, 1);
-            const uint64_t q_desc = smem_desc_sw128(sbase + t * L::Q_TILE, 16, 1024);
+            const uint64_t q_desc = smem_desc_sw128(sbase + (ONE ? 0 : t) * L::Q_TILE, 16, 1024);
             const uint64_t k_desc = smem_desc_sw128(sbase + L::K_OFF, 16, 1024);
             const uint64_t v_desc = smem_desc_sw128(sbase + L::V_OFF, L::KV_CHUNK, 1024);  // V as MN-major B
             auto wait_all = [&](uint32_t bb, uint32_t parity, int site) {
                 return __all_sync(0xFFFFFFFFu, mbar_wait(bb, parity, wc, site)) != 0;
             };
-            // S of step h, whose K has been waited for
-            auto issue_s = [&](int h) {
-                const int st = h % L::STAGES;
-                // behind the P V of step h - 2, which reads this buffer (see the header)
-                if (h >= 2 && leader)
-                    tmem_shift_down(tmem + s_col(t, h & 1));
+            // S of this warp's step i, whose K has been waited for
+            auto issue_s = [&](int i) {
+                const int st = turns.step(i) % L::STAGES;
+                // behind the P V of its step i - 2, which reads this buffer (see the header)
+                if (i >= 2 && leader)
+                    tmem_shift_down(tmem + s_col(t, i & 1));
                 const uint64_t kd = desc_add(k_desc, st * L::KV_TILE);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint64_t ad = desc_add(q_desc, (kk >> 2) * L::Q_CHUNK + (kk & 3) * 32);
                     const uint64_t bd = desc_add(kd, (kk >> 2) * L::KV_CHUNK + (kk & 3) * 32);
-                    mma_ss(leader, tmem + s_col(t, h & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
+                    mma_ss(leader, tmem + s_col(t, i & 1), ad, bd, idesc_s, kk > 0 ? 1u : 0u);
                 }
                 if (leader) {
-                    mma_commit(bar(B_S_FULL + 2 * t + (h & 1)));
+                    mma_commit(bar(B_S_FULL + 2 * t + (i & 1)));
                     mma_commit(bar(B_K_EMPTY + st));
                 }
             };
-            auto wait_k = [&](int h) {
+            auto wait_k = [&](int i) {
+                const int h = turns.step(i);
                 return wait_all(bar(B_K_FULL + h % L::STAGES), (h / L::STAGES) & 1, SITE_K_FULL);
             };
             bool ok = true;
-            for (int h = 0; ok && h < min(n, 2); ++h) {
-                if (!(ok = wait_k(h)))
+            for (int i = 0; ok && i < min(turns.n, 2); ++i) {
+                if (!(ok = wait_k(i)))
                     break;
                 fence_proxy_async_smem();
                 tc_fence_after();
-                issue_s(h);
+                issue_s(i);
             }
-            for (int h = 0; ok && h < n; ++h) {
+            for (int i = 0; ok && i < turns.n; ++i) {
                 // V of this step and K of the step after next first, so that nothing
-                // stands between P and the two products behind it
-                const int st = h % L::STAGES, buf = h & 1;
-                if (!(ok = wait_all(bar(B_V_FULL + st), (h / L::STAGES) & 1, SITE_V_FULL)) ||
-                    !(ok = h + 2 >= n || wait_k(h + 2)))
+                // stands between P and the two products behind it.  (With the steps
+                // taken in turn that K is four steps on: the convert warps reach it
+                // only when this step's P V has left its stage of V.)
+                const int h = turns.step(i), st = h % L::STAGES, buf = i & 1;
+                const bool more = i + 2 < turns.n;
+                ok = wait_all(bar(B_V_FULL + st), (h / L::STAGES) & 1, SITE_V_FULL);
+                if (!ONE && ok && more)
+                    ok = wait_k(i + 2);
+                if (!ok)
                     break;
                 fence_proxy_async_smem();
-                if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (h >> 1) & 1, SITE_P_FULL)))
+                if (!(ok = wait_all(bar(B_P_FULL + 2 * t + buf), (i >> 1) & 1, SITE_P_FULL)))
                     break;
                 tc_fence_after();
                 const uint64_t vd = desc_add(v_desc, st * L::KV_TILE);
 #pragma unroll
                 for (int kk = 0; kk < STEP / 16; ++kk)
                     mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048), idesc_pv,
-                           (h > 0 || kk > 0) ? 1u : 0u);
+                           (i > 0 || kk > 0) ? 1u : 0u);
                 if (leader) {
                     mma_commit(bar(B_PV_DONE + t));
                     mma_commit(bar(B_V_EMPTY + st));
                 }
-                if (h + 2 < n)
-                    issue_s(h + 2);
+                if (more) {
+                    if (ONE) {
+                        if (!(ok = wait_k(i + 2)))
+                            break;
+                        fence_proxy_async_smem();
+                        tc_fence_after();
+                    }
+                    issue_s(i + 2);
+                }
             }
             if (leader)
                 mma_commit(bar(B_O_FINAL + t));
             // Every MMA issued by the elected lane has completed once O_FINAL fires.
             drain_wait(bar(B_O_FINAL + t), 0, p.timeout_ns);
-        } else if (warp == FETCH_WARP && n > 0) {
+        } else if (warp >= FETCH_WARP && n > 0) {
             // ----------------------------------------------------------- fetch
             const int lane = threadIdx.x & 31;
             const long long first = (bh * p.W * p.s + begin) * D;
@@ -399,9 +443,10 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                         scale[i] = __ldg((i < 2 ? p.k_scale : p.v_scale) + scale_index(p, bh, key));
                 }
             };
-            load_scales(0);
-            int issued = 0;
-            for (int hh = 0; hh < n; ++hh) {
+            const int mine = warp - FETCH_WARP;  // the two fetch warps take the steps in turn
+            load_scales(mine);
+            int last = mine - 2;
+            for (int hh = mine; hh < n; hh += 2) {
                 const int rs = hh % L::RAW;
                 if (hh >= L::RAW && !__all_sync(0xFFFFFFFFu, mbar_wait(bar(B_RAW_EMPTY + rs), ((hh / L::RAW) - 1) & 1,
                                                                        wc, SITE_RAW_EMPTY)))
@@ -427,13 +472,14 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                     bulk_load(raw, p.k8 + at, bytes, bar(B_RAW_FULL + rs));
                     bulk_load(raw + L::RAW_TILE, p.v8 + at, bytes, bar(B_RAW_FULL + rs));
                 }
-                issued = hh + 1;
-                if (hh + 1 < n)
-                    load_scales(hh + 1);
+                last = hh;
+                if (hh + 2 < n)
+                    load_scales(hh + 2);
             }
             // Let the copies in flight land before the block can exit: at most the last
             // one of each stage is.
-            for (int j = max(0, issued - L::RAW); j < issued; ++j)
+            static_assert(L::RAW == 4, "two stages a fetch warp");
+            for (int j = max(mine, last - 2); j <= last; j += 2)
                 drain_wait(bar(B_RAW_FULL + j % L::RAW), (j / L::RAW) & 1, p.timeout_ns);
         }
     } else if (warp >= CONVERT_WARP) {
@@ -445,44 +491,62 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         for (int hh = 0; hh < n; ++hh) {
             const int st = hh % L::STAGES, rs = hh % L::RAW;
             const uint32_t freed = ((hh / L::STAGES) - 1) & 1;
-            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_RAW_FULL + rs), (hh / L::RAW) & 1, wc, SITE_RAW_FULL));
+            auto wait_empty = [&](int kv) {
+                return hh < L::STAGES ||
+                       __all_sync(0xFFFFFFFFu, mbar_wait(bar((kv ? B_V_EMPTY : B_K_EMPTY) + st), freed, wc,
+                                                         kv ? SITE_V_EMPTY : SITE_K_EMPTY));
+            };
             const uint8_t* raw = smem + L::RAW_OFF + rs * 2 * L::RAW_TILE;
             const uint32_t* factors =
                 reinterpret_cast<const uint32_t*>(smem + L::FACTOR_OFF) + rs * L::FACTORS;
-#pragma unroll 1
-            for (int kv = 0; ok && kv < 2; ++kv) {  // K, then V
-                if (hh >= L::STAGES)
-                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar((kv ? B_V_EMPTY : B_K_EMPTY) + st), freed, wc,
-                                                           kv ? SITE_V_EMPTY : SITE_K_EMPTY));
-                if (!ok)
-                    break;
+            auto store = [&](const Codes<D>& c, int kv) {
                 uint8_t* stage = smem + (kv ? L::V_OFF : L::K_OFF) + st * L::KV_TILE;
                 if (factors[2 * STEP])
-                    convert<D, true>(raw + kv * L::RAW_TILE, factors + kv * STEP, stage, row, part);
+                    store_codes<D, true>(c, stage, row, part);
                 else
-                    convert<D, false>(raw + kv * L::RAW_TILE, factors + kv * STEP, stage, row, part);
+                    store_codes<D, false>(c, stage, row, part);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(bar((kv ? B_V_FULL : B_K_FULL) + st));
+            };
+            bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_RAW_FULL + rs), (hh / L::RAW) & 1, wc, SITE_RAW_FULL));
+            if (ONE) {  // K and V together: the step is as long as this takes
+                if (!(ok = ok && wait_empty(0) && wait_empty(1)))
+                    break;
+                Codes<D> k, v;
+                load_codes<D>(k, raw, factors, row, part);
+                load_codes<D>(v, raw + L::RAW_TILE, factors + STEP, row, part);
+                store(k, 0);
+                store(v, 1);
+            } else {
+#pragma unroll 1
+                for (int kv = 0; ok && kv < 2; ++kv) {
+                    if (!(ok = wait_empty(kv)))
+                        break;
+                    Codes<D> c;
+                    load_codes<D>(c, raw + kv * L::RAW_TILE, factors + kv * STEP, row, part);
+                    store(c, kv);
+                }
+                if (!ok)
+                    break;
             }
-            if (!ok)
-                break;
             if (lane == 0)
                 mbar_arrive(bar(B_RAW_EMPTY + rs));
         }
-    } else if (warp < 4 * tiles) {
+    } else if (ONE || warp < 4 * tiles) {
         // ------------------------------------------------------------- softmax
         take_registers<SOFTMAX_REGS>();
         const int t = warp >> 2;
-        const int row = q0 + t * TILE_ROWS + (threadIdx.x & 127);
+        const Turns turns = turns_of<ONE>(t, n);
+        const int row = q0 + (ONE ? 0 : t) * TILE_ROWS + (threadIdx.x & 127);
         const bool row_valid = row < p.nq;
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float c = p.scale_log2;
         float m_run = -INFINITY, l_run = 0.f;
         bool ok = true;
-        for (int hh = 0; hh < n; ++hh) {
-            const uint32_t col = s_col(t, hh & 1);
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_S_FULL + 2 * t + (hh & 1)), (hh >> 1) & 1, wc, SITE_S_FULL));
+        for (int i = 0; i < turns.n; ++i) {
+            const uint32_t col = s_col(t, i & 1);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_S_FULL + 2 * t + (i & 1)), (i >> 1) & 1, wc, SITE_S_FULL));
             if (!ok)
                 break;
             tc_fence_after();
@@ -490,7 +554,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             tmem_ld32(lanes + col, s[0]);
             tmem_ld32(lanes + col + 32, s[1]);
             tmem_wait_ld();
-            const int valid = end - (begin + hh * STEP);  // keys of this step
+            const int valid = end - (begin + turns.step(i) * STEP);  // keys of this step
             if (valid < STEP) {
 #pragma unroll
                 for (int e = 0; e < STEP; ++e)
@@ -520,8 +584,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             auto raise_max = [&](float m_step) {
                 const float m_new = fmaxf(m_run, m_step);
                 const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_run - m_new);
-                if (hh > 0) {
-                    raised = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_PV_DONE + t), (hh - 1) & 1, wc, SITE_PV_DONE));
+                if (i > 0) {
+                    raised = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_PV_DONE + t), (i - 1) & 1, wc, SITE_PV_DONE));
                     if (!raised)
                         return;
                     tc_fence_after();
@@ -572,16 +636,53 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             l_run += sum;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(bar(B_P_FULL + 2 * t + (hh & 1)));
+            mbar_arrive(bar(B_P_FULL + 2 * t + (i & 1)));
         }
 
         // ------------------------------------------------------------ epilogue
-        if (n > 0 && ok)
+        if (turns.n > 0 && ok)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_O_FINAL + t), 0, wc, SITE_O_FINAL));
+        // With the steps taken in turn, group 1 leaves its maximum, sum and O
+        // ([column][row]) in the stages, and group 0 joins them to its own.
+        float* other_o = reinterpret_cast<float*>(smem + L::K_OFF) + (threadIdx.x & 127);
+        float* other_ml = reinterpret_cast<float*>(smem + L::RAW_OFF) + (threadIdx.x & 127);
+        const bool join = ONE && n > 1;  // group 1 has had a step
+        if (join) {
+            if (ok)  // the other's products read the stages
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar(B_O_FINAL + 1 - t), 0, wc, SITE_O_FINAL));
+            tc_fence_after();
+            if (t == 1 && ok) {
+                static_assert(!ONE || D * TILE_ROWS * 4 <= 2 * L::STAGES * L::KV_TILE, "O fits the stages");
+                other_ml[0] = m_run;
+                other_ml[TILE_ROWS] = l_run;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t o[32];
+                    tmem_ld32(lanes + o_col(1) + k * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        other_o[(k * 32 + e) * TILE_ROWS] = __uint_as_float(o[e]);
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");  // the two groups, whatever became of them
+        }
         tc_fence_after();
-        if (ok && !*abort_flag) {
+        if (ok && !*abort_flag && (!ONE || t == 0)) {
             const long long at = bh * p.nq + row;
-            const float f = p.splits > 1 ? 1.f : (l_run == 0.f ? 0.f : 1.f / l_run);
+            float mine = 1.f, others = 0.f;  // factors of the joined O
+            if (join) {
+                const float m1 = other_ml[0], m = fmaxf(m_run, m1);
+                mine = m_run == -INFINITY ? 1.f : fast_exp2(m_run - m);  // 1: its sums are 0 or NaN
+                others = m1 == -INFINITY ? 1.f : fast_exp2(m1 - m);
+                l_run = l_run * mine + other_ml[TILE_ROWS] * others;
+                m_run = m;
+            }
+            if (p.splits == 1) {
+                const float f = l_run == 0.f ? 0.f : 1.f / l_run;
+                mine *= f;
+                others *= f;
+            }
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
                 uint32_t o[32];
@@ -597,7 +698,9 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {  // columns 1 and 2 of every four hold channels 2 and 1
                     const int from = (e & 3) == 1 ? e + 1 : ((e & 3) == 2 ? e - 1 : e);
-                    x[e] = __uint_as_float(o[from]) * f;
+                    x[e] = __uint_as_float(o[from]) * mine;
+                    if (join)
+                        x[e] = fmaf(other_o[(k * 32 + from) * TILE_ROWS], others, x[e]);
                 }
                 if (!row_valid)
                     continue;
@@ -633,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     }
 }
 
-template <int D>
+template <int D, bool ONE>
 ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
 {
     // the attribute belongs to the function on one device
@@ -642,13 +745,13 @@ ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
     RA_CUDA_TRY(cudaGetDevice(&dev));
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev >= 64 || !(set.load(std::memory_order_acquire) & bit)) {
-        RA_CUDA_TRY(cudaFuncSetAttribute(cache8_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Layout<D>::SMEM));
+        RA_CUDA_TRY(cudaFuncSetAttribute(cache8_tiles_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Layout<D, ONE>::SMEM));
         if (dev < 64)
             set.fetch_or(bit, std::memory_order_release);
     }
     const dim3 grid(static_cast<unsigned>(p.q_tiles) * p.splits, p.H, B);
-    cache8_tiles_kernel<D><<<grid, THREADS, Layout<D>::SMEM, cs>>>(p);
+    cache8_tiles_kernel<D, ONE><<<grid, THREADS, Layout<D, ONE>::SMEM, cs>>>(p);
     return cuda_fail(cudaGetLastError(), "cache8_tiles_kernel launch");
 }
 
@@ -656,7 +759,9 @@ ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
 
 ra_status cache8_tiles(const AttnParams& p, int B, int d, cudaStream_t cs)
 {
-    return d == 64 ? launch<64>(p, B, cs) : launch<128>(p, B, cs);
+    if (p.nq <= TILE_ROWS)
+        return d == 64 ? launch<64, true>(p, B, cs) : launch<128, true>(p, B, cs);
+    return d == 64 ? launch<64, false>(p, B, cs) : launch<128, false>(p, B, cs);
 }
 
 }  // namespace ra

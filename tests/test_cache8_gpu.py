@@ -396,6 +396,52 @@ def test_non_finite_blocks_stay_where_they_are_read(nq):
     assert not bool(torch.isnan(ra.cache8_attention(q, k8, v8, ks, vs, 4, key_counts=counts)).any())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [17, 64, 128])
+def test_one_tile_of_queries_over_any_number_of_steps(nq, d):
+    """Up to 128 queries share a tile, and its keys are taken in two sequences of
+    64-key steps that are joined at the end: none, one, and more steps in either, with
+    blocks enough that the range of keys does not split."""
+    _gpu.need_gpu()
+    s, W = 64, 11
+    counts = [64 * i + j for i in range(11) for j in (0, 1, 63)]
+    ring, _ = _ring(len(counts), 5, d, s, W, seed=nq + d)
+    q = torch.randn(len(counts), 5, nq, d, device="cuda").bfloat16()
+    _check(q, ring, s, W, counts, what=f"{nq} queries")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B", [1, 80])
+@pytest.mark.parametrize("down", [False, True])
+def test_one_tile_of_queries_whose_maximum_moves(down, B, d):
+    """Keys that grow (or shrink) by 2 ^ 1/2 from step to step: every step raises its
+    sequence's maximum, or adds next to nothing to it."""
+    _gpu.need_gpu()
+    s, W = 64, 11
+    (k8, v8, ks, vs), _ = _ring(B, 2, d, s, W, seed=d + B)
+    ramp = 2.0 ** (torch.arange(W, device="cuda").float() / 2)
+    ks.mul_((ramp.flip(0) if down else ramp)[None, None, :, None])
+    q = torch.randn(B, 2, 100, d, device="cuda").bfloat16()
+    # Every second scale is no power of two: the kernel rounds it, and code * scale, to
+    # bf16 (two roundings, each at most BF16 of the value).  The keys so rounded are bf16
+    # operands whose products are exact again, as _reference's bounds want them.
+    ra = _gpu.ra()
+    lse = torch.empty(B, 2, 100, device="cuda")
+    o = ra.cache8_attention(q, k8, v8, ks, vs, W, lse=lse)
+    true = _values(k8, ks, s)
+    keys = _values(k8, ks.bfloat16(), s).bfloat16()
+    assert bool(((keys.double() - true).abs() <= true.abs() * (2 * _heads.BF16 + _heads.BF16 ** 2)).all())
+    want, want_lse, ob, lb = _reference(q, keys, v8, torch.ones_like(ks), vs, s, [W * s] * B, 1 / math.sqrt(d))
+    off = ((o.double().cpu() - want).abs() / ob).max().item()
+    assert off <= 1, f"o off by {off:.3g} of the bound"
+    off = ((lse.double().cpu() - want_lse).abs() / lb).max().item()
+    assert off <= 1, f"lse off by {off:.3g} of the bound"
+
+
+def test_non_finite_blocks_of_one_tile_of_queries():
+    test_non_finite_blocks_stay_where_they_are_read(70)
+
+
 @pytest.mark.parametrize("nq", [1, 33, 260])
 def test_same_bits_on_any_stream_and_in_a_graph(nq):
     """Two runs, a run on another stream, and a captured graph replayed after the ring
