@@ -477,9 +477,8 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
 
 // How the work is cut.  Few queries: ranges of at least MIN_CHUNK keys, as many as
 // fill the SMs once, or several times where the ranges stay above LONG_CHUNK (batches
-// of unequal lengths balance better).  Many: the number of ranges with the least
-// estimated time, counted in steps of 64 keys of the 256-query kernel (one block an
-// SM).
+// of unequal lengths balance better).  Many: the tiles a block (two, or one) and the
+// number of ranges with the least estimated time, one block an SM.
 constexpr int MIN_CHUNK = 256, LONG_CHUNK = 1024;
 constexpr int WHOLE = 512;  // as many keys as one block takes in less time than the join's launch
 constexpr int SMS = 148;
@@ -490,12 +489,20 @@ constexpr int WANT_BLOCKS = SMS * 16;
 // the few-query kernel takes them in one go with blocks to spare (256 keys, 24 heads
 // of 64, 128 queries: 9.5 against 10.4 us; twice the blocks: 14.5 against 20.7).
 constexpr int FEW_BLOCKS = 192;
-constexpr double STEP_US = 1.0;        // a step of 64 keys: 0.8 us with 64 channels, 1.1 with 128 (one tile: 0.5, 0.8)
-constexpr double START_STEPS = 6;      // a block's start and epilogue, in steps
-constexpr double JOIN_BYTES_PER_US = 5e6;
+// A step of 64 keys, and a block's start and epilogue, as measured with a block on
+// each SM (12480 keys: two tiles 197 us with 64 channels and 231 with 128, one 113 and
+// 171); the join.  One tile a block wins where blocks are scarce or the last tile is
+// alone: 300 queries, 80 heads of 64, 12480 keys 253 -> 214 us; 256 queries, 24 heads
+// of 128, 512 keys 18.7 -> 14.6, but 12480 keys 62 -> 73.
+struct TileCost {
+    int rows;
+    double step64_us, step128_us, start_us;
+};
+constexpr TileCost TILE_COSTS[2] = {{128, 0.55, 0.85, 4}, {256, 1.0, 1.15, 6}};
+constexpr double JOIN_US = 5, JOIN_BYTES_PER_US = 5e6;
 
 struct Plan {
-    bool many;
+    bool many, one;
     int q_tiles, splits, chunk;
     size_t bytes;
 };
@@ -504,24 +511,35 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
 {
     Plan pl;
     pl.many = nq > 2 * COLS && !(nk <= WHOLE && static_cast<long long>((nq + 2 * COLS - 1) / (2 * COLS)) * H * B <= FEW_BLOCKS);
-    const int rows = pl.many ? 256 : (nq <= COLS ? COLS : 2 * COLS), unit = pl.many ? 64 : GROUP * WARPS;
-    pl.q_tiles = (nq + rows - 1) / rows;
-    const long long tiles = static_cast<long long>(pl.q_tiles) * H * B;
+    pl.one = false;
+    const int unit = pl.many ? 64 : GROUP * WARPS;
     long long splits = 1;
     if (pl.many) {
         const long long steps = (static_cast<long long>(nk) + unit - 1) / unit;
-        const double part = static_cast<double>(B) * H * nq * (d + 2) * 4 * 2 / JOIN_BYTES_PER_US / STEP_US;
-        double best = 0;
-        for (long long k = 1; k <= 32 && k * 4 <= (steps > 4 ? steps : 4); ++k) {
-            const double rounds = static_cast<double>((tiles * k + SMS - 1) / SMS);
-            const double cost = rounds * (static_cast<double>((steps + k - 1) / k) + START_STEPS) +
-                                (k > 1 ? part * static_cast<double>(k) + 5 : 0);
-            if (k == 1 || cost < best) {
-                best = cost;
-                splits = k;
+        const double part = static_cast<double>(B) * H * nq * (d + 2) * 4 * 2 / JOIN_BYTES_PER_US;
+        double best = -1;
+        for (const TileCost& c : TILE_COSTS) {
+            const int q_tiles = (nq + c.rows - 1) / c.rows;
+            const long long tiles = static_cast<long long>(q_tiles) * H * B;
+            if (c.rows == 256 && nq <= 128)
+                break;
+            for (long long k = 1; k <= 32 && k * 4 <= (steps > 4 ? steps : 4); ++k) {
+                const double rounds = static_cast<double>((tiles * k + SMS - 1) / SMS);
+                const double step = d == 64 ? c.step64_us : c.step128_us;
+                const double cost = rounds * (static_cast<double>((steps + k - 1) / k) * step + c.start_us) +
+                                    (k > 1 ? part * static_cast<double>(k) + JOIN_US : 0);
+                if (best < 0 || cost < best) {
+                    best = cost;
+                    splits = k;
+                    pl.q_tiles = q_tiles;
+                    pl.one = c.rows == 128;
+                }
             }
         }
     } else {
+        const int rows = nq <= COLS ? COLS : 2 * COLS;
+        pl.q_tiles = (nq + rows - 1) / rows;
+        const long long tiles = static_cast<long long>(pl.q_tiles) * H * B;
         const long long one_wave = (ONE_WAVE + tiles - 1) / tiles, waves = (WANT_BLOCKS + tiles - 1) / tiles;
         const long long long_chunks = nk / LONG_CHUNK;
         splits = waves < long_chunks ? waves : long_chunks;
@@ -638,7 +656,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (pl.many) {
         p.timeout_ns = wait_timeout_ns();
-        if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, cs)) != RA_OK)
+        if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, pl.one, cs)) != RA_OK)
             return st;
     } else {
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);

@@ -1,8 +1,8 @@
 // ra_cache8_tiles.cu -- attention of many queries over the 8-bit key/value ring
 // on the tensor cores (tcgen05, accumulators in TMEM).
 //
-// One CTA per (head, 256 queries, range of keys), one CTA per SM, keys in steps
-// of 64.  Five warpgroups in fixed roles:
+// One CTA per (head, 256 queries, range of keys), or 128 queries (see ONE below), one
+// CTA per SM, keys in steps of 64.  Five warpgroups in fixed roles:
 //   warps 0-3, 4-7  softmax of query tile 0 and 1 (128 rows each): thread t of the
 //                   group owns row t (TMEM lane t); per step reads S, keeps the
 //                   running maximum and sum, writes P (bf16) back over S; at the end
@@ -29,7 +29,8 @@
 // waits, 100-200 clocks each, stood between one tile's products and the other's), four
 // convert warps 918.
 //
-// Up to 128 queries are one tile (ONE).  Its steps are taken in turn by the two
+// Up to 128 queries, and more where that is sooner done, are one tile a block (ONE).
+// Its steps are taken in turn by the two
 // softmax groups and MMA warps, each with its own maximum, sum and O, which group 0
 // joins to its own at the end.  With one group at work and one fetch warp a step took
 // 1700 clocks; turns alone changed nothing, a fetch warp's own chain (waits, indexes,
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     if (p.splits > 1 && begin >= count)
         return;  // the join does not read this split
     const int end = min(begin + p.chunk, count);
-    const int q0 = q_tile * 2 * TILE_ROWS;
+    const int q0 = q_tile * (ONE ? 1 : 2) * TILE_ROWS;
     const int tiles = !ONE && p.nq - q0 > TILE_ROWS ? 2 : 1;
     WaitCtl wc{abort_flag, p.err, p.timeout_ns};
     if (p.splits > 1)
@@ -757,9 +758,9 @@ ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
 
 }  // namespace
 
-ra_status cache8_tiles(const AttnParams& p, int B, int d, cudaStream_t cs)
+ra_status cache8_tiles(const AttnParams& p, int B, int d, bool one, cudaStream_t cs)
 {
-    if (p.nq <= TILE_ROWS)
+    if (one)
         return d == 64 ? launch<64, true>(p, B, cs) : launch<128, true>(p, B, cs);
     return d == 64 ? launch<64, false>(p, B, cs) : launch<128, false>(p, B, cs);
 }

@@ -438,6 +438,19 @@ def test_one_tile_of_queries_whose_maximum_moves(down, B, d):
     assert off <= 1, f"lse off by {off:.3g} of the bound"
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,nq,s", [(4, 37, 200, 60), (2, 3, 300, 60), (4, 37, 129, 60), (2, 74, 257, 130), (1, 2, 513, 200)])
+def test_one_and_two_tiles_of_queries_a_block(B, H, nq, s, d):
+    """Heads enough to fill the SMs with blocks of two tiles, or few, with tiles of a few
+    rows at the end."""
+    _gpu.need_gpu()
+    W = 10
+    counts = [s * W - 7 * b for b in range(B)]
+    ring, _ = _ring(B, H, d, s, W, seed=nq)
+    q = torch.randn(B, H, nq, d, device="cuda").bfloat16()
+    _check(q, ring, s, W, counts, what=f"{nq} queries")
+
+
 def test_non_finite_blocks_of_one_tile_of_queries():
     test_non_finite_blocks_stay_where_they_are_read(70)
 
