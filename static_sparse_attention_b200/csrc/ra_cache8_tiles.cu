@@ -669,7 +669,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             asm volatile("bar.sync 1, 256;" ::: "memory");  // the two groups, whatever became of them
         }
         tc_fence_after();
-        if (ok && !*abort_flag && (!ONE || t == 0)) {
+        // one answer a warp: the flag may rise between two lanes' looks at it
+        if (__all_sync(0xFFFFFFFFu, ok && !*abort_flag) && (!ONE || t == 0)) {
             const long long at = bh * p.nq + row;
             float mine = 1.f, others = 0.f;  // factors of the joined O
             if (join) {
@@ -686,6 +687,9 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
             }
 #pragma unroll
             for (int k = 0; k < D / 32; ++k) {
+                // The stores of the round before part the lanes of a tile's last, ragged warp; the
+                // load is warp-collective (.sync.aligned) and undefined in a warp that is not whole.
+                __syncwarp();
                 uint32_t o[32];
                 if (n > 0) {
                     tmem_ld32(lanes + o_col(t) + k * 32, o);
