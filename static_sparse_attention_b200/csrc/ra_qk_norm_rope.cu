@@ -247,10 +247,47 @@ ra_status check_strides(const char* what, long long* sb, long long* sn, long lon
     return RA_OK;
 }
 
-// Whether the strided tensors dq and dk (bf16 elements) certainly share none:
-// apart altogether, or slots of one packed buffer -- of each token's row (the
-// output of a fused projection, [B, n, Hq + Hk + .., d]) or of each head's
-// ([B, n, H, 3, d]).
+// Whether blocks of `row` contiguous elements, one for each index of up to four
+// dimensions, certainly share none: sorted by stride, each dimension steps over the
+// whole of the ones below it.
+struct Dim {
+    long long stride;
+    int size;
+};
+template <int N>
+bool blocks_disjoint(Dim (&dims)[N], long long row)
+{
+    for (int i = 0; i < N; ++i)
+        for (int j = i + 1; j < N; ++j)
+            if (dims[j].stride < dims[i].stride ||
+                (dims[j].stride == dims[i].stride && dims[j].size < dims[i].size)) {
+                const Dim a = dims[i];
+                dims[i] = dims[j];
+                dims[j] = a;
+            }
+    long long below = row;
+    for (const Dim& dim : dims) {
+        if (dim.size == 1)
+            continue;
+        if (dim.stride < below)
+            return false;
+        below = dim.stride * (dim.size - 1) + below;
+    }
+    return true;
+}
+
+// The rows of a strided output.
+bool rows_disjoint(const Rows& t, int B, int n, int d)
+{
+    Dim dims[3] = {{t.gb, B}, {t.gn, n}, {t.gh, t.H}};
+    return blocks_disjoint(dims, d);
+}
+
+// Whether the strided tensors dq and dk (bf16 elements), the rows of each disjoint,
+// certainly share none: apart altogether, or slots of one packed buffer -- of each
+// token's row (the output of a fused projection, [B, n, Hq + Hk + .., d]), or with as
+// many heads of the same stride, dk as dq's second index ([B, n, H, 2 or 3, d],
+// [B, 2 H, n, d] and the like).
 bool grads_disjoint(const Rows& q, const Rows& k, int B, int n, int d)
 {
     const uintptr_t a = reinterpret_cast<uintptr_t>(q.dx), c = reinterpret_cast<uintptr_t>(k.dx);
@@ -260,36 +297,12 @@ bool grads_disjoint(const Rows& q, const Rows& k, int B, int n, int d)
         return false;
     const long long apart = static_cast<long long>(a < c ? c - a : a - c) / 2;
     const Rows &lo = a < c ? q : k, &hi = a < c ? k : q;
-    const long long lo_end = (lo.H - 1) * lo.gh + d, hi_end = apart + (hi.H - 1) * hi.gh + d;
-    const long long step = n > 1 && (B == 1 || q.gn <= q.gb) ? q.gn : (B > 1 ? q.gb : hi_end);
-    if (apart >= lo_end && hi_end <= step)
+    // a token's slots as one block, from the first one's start to the second one's end
+    Dim tokens[2] = {{q.gb, B}, {q.gn, n}};
+    if (apart >= (lo.H - 1) * lo.gh + d && blocks_disjoint(tokens, apart + (hi.H - 1) * hi.gh + d))
         return true;
-    return q.gh == k.gh && q.H == k.H && apart >= d && apart + d <= q.gh;
-}
-
-// Rows of a strided output must not share elements: sorted by stride, each
-// dimension steps over the whole of the ones below it.
-bool rows_disjoint(long long sb, long long sn, long long sh, int B, int n, int H, int d)
-{
-    long long s[3] = {sb, sn, sh};
-    int size[3] = {B, n, H};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 3; ++j)
-            if (s[j] < s[i] || (s[j] == s[i] && size[j] < size[i])) {
-                const long long a = s[i];
-                s[i] = s[j], s[j] = a;
-                const int c = size[i];
-                size[i] = size[j], size[j] = c;
-            }
-    long long below = d;
-    for (int i = 0; i < 3; ++i) {
-        if (size[i] == 1)
-            continue;
-        if (s[i] < below)
-            return false;
-        below = s[i] * (size[i] - 1) + below;
-    }
-    return true;
+    Dim rows[4] = {{q.gb, B}, {q.gn, n}, {q.gh, q.H}, {apart, 2}};
+    return q.gh == k.gh && q.H == k.H && blocks_disjoint(rows, d);
 }
 
 }  // namespace
@@ -527,7 +540,7 @@ extern "C" ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_ro
         t.gh = g->stride_h;
         if ((st = check_strides(name[i], &t.gb, &t.gn, &t.gh, B, n, t.H)) != RA_OK)
             return st;
-        if (n > 0 && !rows_disjoint(t.gb, t.gn, t.gh, B, n, t.H, d))
+        if (n > 0 && !rows_disjoint(t, B, n, d))
             return fail(RA_ERR_INVALID_ARG, "%s: rows of an output overlap", name[i]);
         t.dy = static_cast<const __nv_bfloat16*>(g->dy);
         t.dx = static_cast<__nv_bfloat16*>(g->dx);
