@@ -485,9 +485,10 @@ class SwcCache8:
     window of SwcCache in half its memory, fed with the projections' rows, which
     are normed and rotated on the way.
 
-    k8, v8, k_scale and v_scale are the ring's buffers (see cache8_append).  Steps
-    must be ordered on one stream, and are refused while it is being captured into a
-    CUDA graph (a replay would repeat one frame number): capture cache8_append and
+    k8, v8, k_scale and v_scale are the ring's buffers (see cache8_append).  Creation
+    is synchronous.  Steps must be ordered on one stream (any one; the buffers' memory
+    is reused behind its work), and are refused while it is being captured into a CUDA
+    graph (a replay would repeat one frame number): capture cache8_append and
     cache8_attention there instead."""
 
     def __init__(self, B: int, H: int, d: int, s: int, window_frames: int):
@@ -502,7 +503,20 @@ class SwcCache8:
                             .view(torch.float8_e4m3fn) for _ in range(2))
         self.k_scale, self.v_scale = (torch.ones((B, H, window_frames, -(-s // CACHE8_BLOCK)), device="cuda")
                                       for _ in range(2))
+        # the fills are on the current stream, the steps on whatever stream they are given
+        self._streams = {_stream_handle(None)}
+        torch.cuda.current_stream().synchronize()
         self.frames_seen = 0
+
+    def _used_on(self, stream) -> None:
+        """Have the allocator reuse the ring's memory only behind the work of `stream`."""
+        handle = _stream_handle(stream)
+        if handle not in self._streams:
+            import torch
+            other = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+            for t in self._ring:
+                t.record_stream(other)
+            self._streams.add(handle)
 
     @property
     def frames_held(self) -> int:
@@ -524,12 +538,14 @@ class SwcCache8:
             raise ValueError(f"k and v must have shape [{self.B}, frames * {self.s}, {self.H}, {self.d}]")
         frames = k.shape[1] // self.s
         skip = max(0, frames - self.W)
+        self._used_on(stream)
         cache8_append(k[:, skip * self.s:], v[:, skip * self.s:], *self._ring, self.frames_seen + skip, k_weight, rope,
                       eps, stream)
         self.frames_seen += frames
 
     def attend(self, q, out=None, lse=None, scale: float | None = None, workspace=None, stream=None):
         """Attention of q (bf16 [B, H, nq, d]) over every token of the frames held."""
+        self._used_on(stream)
         return cache8_attention(q, *self._ring, self.frames_held, None, scale, out, lse, workspace, stream)
 
     def step(self, q, k, v, q_weight=None, k_weight=None, rope=None, eps: float = 1e-6, out=None, lse=None,
