@@ -363,6 +363,9 @@ ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, cons
  *   workspace  : caller-owned device memory of ra_cache8_attention_workspace_bytes
  *                for the same sizes (0 for some), 16-byte aligned; calls that may
  *                overlap on the GPU need one each.
+ * ra_cache8_attention_check -- whether ra_cache8_attention would take these
+ *   arguments; launches nothing.  For a caller that appends a frame first and must
+ *   not find the attention refused behind it.
  * No output may alias another buffer of the call.  Deterministic (no atomics);
  * asynchronous on `stream`; no allocation, so the calls may be captured into a CUDA
  * graph (which replays them with the same frame and held).
@@ -376,6 +379,10 @@ ra_status ra_cache8_attention(const void* Q, const void* k8, const void* v8, con
                               const float* v_scale, void* O, int B, int H, int d, int nq, int s, int window_frames,
                               int held, const int* key_counts, float scale, float* lse, void* workspace,
                               size_t workspace_bytes, ra_stream stream);
+ra_status ra_cache8_attention_check(const void* Q, const void* k8, const void* v8, const float* k_scale,
+                                    const float* v_scale, const void* O, int B, int H, int d, int nq, int s,
+                                    int window_frames, int held, const int* key_counts, float scale, const float* lse,
+                                    const void* workspace, size_t workspace_bytes);
 
 /* Synchronise `stream`, then read and clear the current device's error word.
  * RA_ERR_DEVICE_TIMEOUT if a kernel gave up a bounded wait since the last call. */

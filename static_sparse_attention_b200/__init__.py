@@ -107,6 +107,8 @@ _SIGS = {
     "ra_cache8_attention_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)], _i),
     "ra_cache8_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
                              ctypes.c_size_t, _vp], _i),
+    "ra_cache8_attention_check": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
+                                   ctypes.c_size_t], _i),
     "ra_get_device_status": ([_vp], _i),
     "ra_get_device_error_site": ([ctypes.POINTER(_i), ctypes.POINTER(_i)], _i),
     "ra_selftest_wait_timeout": ([_ll, _vp], _i),
@@ -414,7 +416,7 @@ def _load_binding():
         from . import _torch_binding as module
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                       (ra_qk_norm_rope, ra_qk_norm_rope_bwd_workspace_bytes, ra_qk_norm_rope_bwd, ra_cache8_append,
-                       ra_cache8_attention_workspace_bytes, ra_cache8_attention)))
+                       ra_cache8_attention_workspace_bytes, ra_cache8_attention, ra_cache8_attention_check)))
         _binding = module
     return _binding
 
@@ -551,7 +553,8 @@ class SwcCache8:
     def step(self, q, k, v, q_weight=None, k_weight=None, rope=None, eps: float = 1e-6, out=None, lse=None,
              scale: float | None = None, stream=None):
         """Feed the next frame (q, k, v: bf16 [B, s, H, d], the projections' rows);
-        returns its output, bf16 [B, H, s, d]."""
+        returns its output, bf16 [B, H, s, d].  A step that raises feeds nothing: the
+        attention's arguments are checked and its buffers allocated before the append."""
         _refuse_capture(stream)
         if tuple(q.shape) != (self.B, self.s, self.H, self.d) or q.shape != k.shape:
             raise ValueError(f"q, k and v must have shape [{self.B}, {self.s}, {self.H}, {self.d}]")
@@ -560,8 +563,18 @@ class SwcCache8:
                 q = q.transpose(1, 2).contiguous()
         else:
             q, _ = qk_norm_rope(q, None, q_weight, None, rope, self.frames_seen, eps, stream=stream)
+        r = (_binding or _load_binding()).cache8_attention_prepare(
+            q, *self._ring, min(self.frames_seen + 1, self.W), None, scale, out, lse, None,
+            None if stream is None else _stream_handle(stream))
+        if type(r) is int:
+            check(r, "ra_cache8_attention")
+        out, workspace = r
         self.append(k, v, k_weight, rope, eps, stream)
-        return self.attend(q, out, lse, scale, stream=stream)
+        try:
+            return self.attend(q, out, lse, scale, workspace, stream)
+        except Exception:
+            self.frames_seen -= 1  # the launch failed: the next step takes the same slot
+            raise
 
     def reset(self) -> None:
         """Forget every frame (the next one is frame 0)."""

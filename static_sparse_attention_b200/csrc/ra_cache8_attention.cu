@@ -593,10 +593,10 @@ extern "C" ra_status ra_cache8_attention_workspace_bytes(int B, int H, int d, in
     return st;
 }
 
-extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const void* v8, const float* k_scale,
-                                         const float* v_scale, void* O, int B, int H, int d, int nq, int s,
-                                         int window_frames, int held, const int* key_counts, float scale, float* lse,
-                                         void* workspace, size_t workspace_bytes, ra_stream stream)
+extern "C" ra_status ra_cache8_attention_check(const void* Q, const void* k8, const void* v8, const float* k_scale,
+                                               const float* v_scale, const void* O, int B, int H, int d, int nq, int s,
+                                               int window_frames, int held, const int* key_counts, float scale,
+                                               const float* lse, const void* workspace, size_t workspace_bytes)
 {
     ra_status st = check_attention(B, H, d, nq, s, window_frames, held);
     if (st != RA_OK || (st = check_cache8(k8, v8, k_scale, v_scale, B, H, d, s, window_frames)) != RA_OK)
@@ -628,6 +628,20 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
             if (overlap(out[i], out[j]))
                 return fail(RA_ERR_INVALID_ARG, "an output may not alias another buffer of the call");
     }
+    return RA_OK;
+}
+
+extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const void* v8, const float* k_scale,
+                                         const float* v_scale, void* O, int B, int H, int d, int nq, int s,
+                                         int window_frames, int held, const int* key_counts, float scale, float* lse,
+                                         void* workspace, size_t workspace_bytes, ra_stream stream)
+{
+    ra_status st = ra_cache8_attention_check(Q, k8, v8, k_scale, v_scale, O, B, H, d, nq, s, window_frames, held,
+                                             key_counts, scale, lse, workspace, workspace_bytes);
+    if (st != RA_OK)
+        return st;
+    const Plan pl = plan_of(B, H, d, nq, held * s);
+    const long long rows = static_cast<long long>(B) * H * nq;
     AttnParams p;
     std::memset(&p, 0, sizeof p);
     p.Q = static_cast<const __nv_bfloat16*>(Q);
@@ -642,7 +656,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     p.nq = nq;
     p.s = s;
     p.W = window_frames;
-    p.blocks = blocks;
+    p.blocks = cache8_blocks(s);
     p.nk = held * s;
     p.per_s = s == 1 ? 0xFFFFFFFFu : static_cast<uint32_t>((1ULL << 32) / static_cast<unsigned>(s));
     p.q_tiles = pl.q_tiles;

@@ -29,6 +29,7 @@ decltype(&ra_qk_norm_rope_bwd) f_qk_norm_rope_bwd;
 decltype(&ra_cache8_append) f_cache8_append;
 decltype(&ra_cache8_attention_workspace_bytes) f_cache8_attention_workspace_bytes;
 decltype(&ra_cache8_attention) f_cache8_attention;
+decltype(&ra_cache8_attention_check) f_cache8_attention_check;
 
 constexpr int64_t CACHE8_BLOCK = 64;
 
@@ -362,11 +363,9 @@ PyObject* cache8_append(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     END_HANDLE_TH_ERRORS
 }
 
-// q, k8, v8, k_scale, v_scale, held, key_counts, scale, out, lse, workspace, stream
-PyObject* cache8_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+// The attention, or (launch false) all of its checks and allocations: returns out, or (out, workspace).
+PyObject* cache8_attention_of(PyObject* const* a, bool launch)
 {
-    HANDLE_TH_ERRORS
-    arguments(n_args, 12);
     const at::Tensor &q = tensor(a[0], "q"), &k8 = tensor(a[1], "k8"), &v8 = tensor(a[2], "v8"),
                      &ks = tensor(a[3], "k_scale"), &vs = tensor(a[4], "v_scale");
     const at::Tensor *counts = tensor_or_none(a[6], "key_counts"), *lse = tensor_or_none(a[9], "lse");
@@ -384,6 +383,7 @@ PyObject* cache8_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args)
                                lse->size(1) == r.H && lse->size(2) == nq && lse->is_contiguous()),
                       "lse must be a contiguous fp32 tensor [B, H, nq] on the inputs' device");
     const at::Tensor out = output(tensor_or_none(a[8], "out"), "out", {r.B, r.H, nq, r.d}, at::kBFloat16, w);
+    at::Tensor ws;
     if (nq) {
         const int B = size_of(r.B, "B"), H = size_of(r.H, "H"), d = size_of(r.d, "d"), s = size_of(r.s, "s"),
                   W = size_of(r.W, "W"), n = size_of(nq, "nq"), held = int_of(a[5], "held");
@@ -391,18 +391,39 @@ PyObject* cache8_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         ra_status st = f_cache8_attention_workspace_bytes(B, H, d, n, s, W, held, &need);
         if (st != RA_OK)
             return PyLong_FromLong(st);
-        const at::Tensor ws = workspace_of(tensor_or_none(a[10], "workspace"), need, w);
+        ws = workspace_of(tensor_or_none(a[10], "workspace"), need, w);
         const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(r.d)) : number(a[7]);
-        st = f_cache8_attention(q.const_data_ptr(), k8.const_data_ptr(), v8.const_data_ptr(),
-                                static_cast<const float*>(ks.const_data_ptr()),
-                                static_cast<const float*>(vs.const_data_ptr()), address(out), B, H, d, n, s, W, held,
-                                counts ? static_cast<const int*>(counts->const_data_ptr()) : nullptr,
-                                static_cast<float>(scale), lse ? static_cast<float*>(lse->mutable_data_ptr()) : nullptr,
-                                address(ws), need, reinterpret_cast<ra_stream>(w.stream));
+        const void *Q = q.const_data_ptr(), *K = k8.const_data_ptr(), *V = v8.const_data_ptr();
+        const float *k_scale = static_cast<const float*>(ks.const_data_ptr()),
+                    *v_scale = static_cast<const float*>(vs.const_data_ptr());
+        const int* key_counts = counts ? static_cast<const int*>(counts->const_data_ptr()) : nullptr;
+        float* lse_at = lse ? static_cast<float*>(lse->mutable_data_ptr()) : nullptr;
+        st = launch ? f_cache8_attention(Q, K, V, k_scale, v_scale, address(out), B, H, d, n, s, W, held, key_counts,
+                                         static_cast<float>(scale), lse_at, address(ws), need,
+                                         reinterpret_cast<ra_stream>(w.stream))
+                    : f_cache8_attention_check(Q, K, V, k_scale, v_scale, address(out), B, H, d, n, s, W, held,
+                                               key_counts, static_cast<float>(scale), lse_at, address(ws), need);
         if (st != RA_OK)
             return PyLong_FromLong(st);
     }
-    return wrap(out);
+    return launch ? wrap(out) : tuple_of({out, ws});
+}
+
+// q, k8, v8, k_scale, v_scale, held, key_counts, scale, out, lse, workspace, stream
+PyObject* cache8_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    arguments(n_args, 12);
+    return cache8_attention_of(a, true);
+    END_HANDLE_TH_ERRORS
+}
+
+// The same arguments: (out, workspace) for a call that will not be refused
+PyObject* cache8_attention_prepare(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    HANDLE_TH_ERRORS
+    arguments(n_args, 12);
+    return cache8_attention_of(a, false);
     END_HANDLE_TH_ERRORS
 }
 
@@ -410,9 +431,10 @@ PyObject* cache8_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     HANDLE_TH_ERRORS
-    arguments(n_args, 6);
-    void* at[6];
-    for (int i = 0; i < 6; ++i) {
+    constexpr int N = 7;
+    arguments(n_args, N);
+    void* at[N];
+    for (int i = 0; i < N; ++i) {
         at[i] = PyLong_AsVoidPtr(a[i]);
         TORCH_CHECK_VALUE(at[i] && !PyErr_Occurred(), "an entry point's address is missing");
     }
@@ -422,13 +444,19 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     f_cache8_append = reinterpret_cast<decltype(f_cache8_append)>(at[3]);
     f_cache8_attention_workspace_bytes = reinterpret_cast<decltype(f_cache8_attention_workspace_bytes)>(at[4]);
     f_cache8_attention = reinterpret_cast<decltype(f_cache8_attention)>(at[5]);
+    f_cache8_attention_check = reinterpret_cast<decltype(f_cache8_attention_check)>(at[6]);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
 
 #define METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD(bind),          METHOD(qk_norm_rope),     METHOD(qk_norm_rope_bwd),
-                         METHOD(cache8_append), METHOD(cache8_attention), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD(bind),
+                         METHOD(qk_norm_rope),
+                         METHOD(qk_norm_rope_bwd),
+                         METHOD(cache8_append),
+                         METHOD(cache8_attention),
+                         METHOD(cache8_attention_prepare),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -66,3 +66,33 @@ def test_the_ring_outlives_its_object_until_the_stream_is_done():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_a_refused_step_leaves_the_ring_as_it_was():
+    """Whatever a step refuses, the ring keeps every bit and the frame's number; the
+    stream goes on as if the refused step had not been."""
+    _gpu.need_gpu()
+    ra = _gpu.ra()
+    B, H, d, s, W = 1, 2, 64, 70, 3
+    frames = _frames(B, H, d, s, 5)
+    w = torch.ones(d, device="cuda")
+    rope = ra.rope3d(5, 7, 10, d)
+    plain, cache = ra.SwcCache8(B, H, d, s, W), ra.SwcCache8(B, H, d, s, W)
+    inside = cache.k8.view(torch.uint8).view(-1)[:2 * B * H * s * d].view(torch.bfloat16).view(B, H, s, d)
+    for i, (q, k, v) in enumerate(frames):
+        before = _bits(cache)
+        for bad, error in ((dict(lse=torch.empty(B, H, s + 1, device="cuda")), ValueError),
+                           (dict(out=torch.empty(B, H, s, d, device="cuda")), ValueError),
+                           (dict(out=inside), ra.RaError),
+                           (dict(scale=0.0), ra.RaError), (dict(scale=float("inf")), ra.RaError),
+                           (dict(eps=0.0), ra.RaError), (dict(k_weight=w[:8]), ValueError)):
+            with pytest.raises(error):
+                cache.step(q, k, v, **{**dict(q_weight=w, k_weight=w, rope=rope), **bad})
+        with pytest.raises(ValueError):
+            cache.step(q, k, v.float(), w, w, rope)
+        assert cache.info == dict(frames_seen=i, frames_held=min(i, W))
+        assert all(torch.equal(a, b) for a, b in zip(before, _bits(cache)))
+        assert torch.equal(cache.step(q, k, v, w, w, rope), plain.step(q, k, v, w, w, rope))
+    with pytest.raises(ra.RaError):  # frame 5 of a table of 5
+        cache.step(q, k, v, w, w, rope)
+    assert cache.frames_seen == 5
