@@ -357,9 +357,9 @@ ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, cons
  *   key_counts : NULL, or device int32 [B]: batch element b attends to the first
  *                key_counts[b] rows only (clamped to [0, held * s]).
  *   lse        : NULL, or device fp32 [B, H, nq] (natural log).
- *   A query without keys gets O = 0 and lse = -inf.  P is rounded to bf16 for its
- *   product with V whatever ra_set_pv_precision says: at 2^-8 of a weight that is
- *   far below the codes' own rounding, 2^-4 of a value.
+ *   A query without keys gets O = 0 and lse = -inf.  P is held for its product with
+ *   V as ra_set_pv_precision says, by the held * s keys of a query (for nq <= 4 as
+ *   hi + lo in any case, which costs no second product there).
  *   workspace  : caller-owned device memory of ra_cache8_attention_workspace_bytes
  *                for the same sizes (0 for some), 16-byte aligned; calls that may
  *                overlap on the GPU need one each.
@@ -412,9 +412,10 @@ ra_status ra_set_wait_timeout_ns(long long timeout_ns);
 
 /* Precision of P in the P V product (process-wide setting).
  *   RA_PV_AUTO   (default) bf16 P, except for masks whose rows average fewer
- *                than 4096 computed keys: there P is held as a hi + lo pair of
- *                bf16 numbers and P V runs as two MMAs, because over few keys the
- *                rounding of each weight to bf16 is not averaged out.
+ *                than 4096 computed keys, and rings of fewer held: there P is held
+ *                as a hi + lo pair of bf16 numbers and P V runs as two MMAs, because
+ *                over few keys the rounding of each weight to bf16 is not averaged
+ *                out.
  *   RA_PV_BF16   always bf16 P (one MMA).
  *   RA_PV_SPLIT  always hi + lo P (two MMAs).
  * INVALID_ARG for any other value. */

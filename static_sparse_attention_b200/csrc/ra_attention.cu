@@ -714,6 +714,12 @@ extern "C" ra_status ra_attention_fwd(const void* Q, const void* K, const void* 
 }
 
 namespace ra {
+bool split_p(long long keys)
+{
+    const int policy = g_pv_policy.load(std::memory_order_relaxed);
+    return policy == RA_PV_SPLIT || (policy == RA_PV_AUTO && keys < SPLIT_P_MAX_KEYS_PER_ROW);
+}
+
 ra_status attention_fwd_rect(const void* Q, const void* K, const void* V, void* O, int B, int H, int d, int nq,
                              int nk, int k_head_rows, const int* row_ptr, const int* col_idx,
                              const unsigned char* flag, int nbq, int nnz, float scale, float* lse, cudaStream_t cs)
@@ -744,8 +750,7 @@ ra_status attention_fwd_rect(const void* Q, const void* K, const void* V, void* 
     p.lse = lse;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.timeout_ns = wait_timeout_ns();
-    const int policy = g_pv_policy.load(std::memory_order_relaxed);
-    const bool split = policy == RA_PV_SPLIT || (policy == RA_PV_AUTO && nk < SPLIT_P_MAX_KEYS_PER_ROW);
+    const bool split = split_p(nk);
     if (d == 64)
         return split ? launch_fwd<64, true>(mq, mk, mv, p, B, cs) : launch_fwd<64, false>(mq, mk, mv, p, B, cs);
     return split ? launch_fwd<128, true>(mq, mk, mv, p, B, cs) : launch_fwd<128, false>(mq, mk, mv, p, B, cs);

@@ -13,7 +13,10 @@
 //        fp16 by a power of two for each query, and the key's scale multiplies the
 //        score.
 //   P V: the values go to bf16 code * scale (ra_cache8.cuh) and P to bf16, whose
-//        range no mixture of scales leaves.
+//        range no mixture of scales leaves, with or without what the rounding leaves
+//        (PForm).  For up to four queries the rests ride in the product's free
+//        columns: one query on 8 x 32768 keys 182 us, without them 179; a second
+//        product 197.  For eight it is a second product, asked for below 4096 keys.
 // Ranges of keys leave partial (maximum, sum, O) to a second kernel that joins them.
 // Bound by memory for few queries (one byte a value of K and V): one query on each of
 // eight caches of 4096 to 32768 keys, 24 heads of 128, 179 us = 5.2 TB/s, 80 % of the
@@ -47,6 +50,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// What the rounding to the pair of bf16 numbers `rounded` leaves of lo and hi.
+__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t rounded)
+{
+    return pack2(lo - __uint_as_float(rounded << 16), hi - __uint_as_float(rounded & 0xFFFF0000u));
 }
 
 // D += A B: A 16 x 16 (row), B 16 x 8 (column), fp32 sums.
@@ -185,8 +194,13 @@ struct State {
     float m[NT][2], l[NT][2];   // l: this lane's keys only
 };
 
+// How P reaches its product with V: rounded to bf16; as that and what the rounding
+// leaves (to 2^-16 of a weight), in two products; or, for up to four queries, in one,
+// whose columns 4-7 are free for the rests of columns 0-3.
+enum PForm { P_BF16, P_PAIR, P_COLUMNS };
+
 // TWO: some scale of the group needs its second factor.
-template <int D, int NT, bool TWO>
+template <int D, int NT, PForm P, bool TWO>
 __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, int key0, int end)
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -244,6 +258,7 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
         }
     }
     uint32_t b0[NT], b1[NT];  // P^T: keys 2 c, 2 c + 1 (b0) and 8 more (b1) of query r
+    uint32_t l0[NT], l1[NT];  // P_PAIR: the rests
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -251,8 +266,19 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
             s[t][e] = exp2_fast(s[t][e] - use[t][e & 1]);
             st.l[t][e & 1] += s[t][e];
         }
-        b0[t] = transpose8x8(pack2(s[t][0], s[t][1]));
-        b1[t] = transpose8x8(pack2(s[t][2], s[t][3]));
+        uint32_t x0 = pack2(s[t][0], s[t][1]), x1 = pack2(s[t][2], s[t][3]);
+        if (P != P_BF16) {
+            const uint32_t y0 = rest2(s[t][0], s[t][1], x0), y1 = rest2(s[t][2], s[t][3], x1);
+            if (P == P_PAIR) {
+                l0[t] = transpose8x8(y0);
+                l1[t] = transpose8x8(y1);
+            } else if (c >= 2) {  // queries 4-7 are queries 0-3 again
+                x0 = y0;
+                x1 = y1;
+            }
+        }
+        b0[t] = transpose8x8(x0);
+        b1[t] = transpose8x8(x1);
     }
     const CodeScale mine = code_scale(g.scale);
     const uint32_t both = mine.first | (mine.second << 16);
@@ -280,8 +306,11 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
             }
         }
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {
             mma_bf16(st.o[i][t], a, b0[t], b1[t]);
+            if (P == P_PAIR)
+                mma_bf16(st.o[i][t], a, l0[t], l1[t]);
+        }
     }
 }
 
@@ -290,7 +319,7 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
 // an SM of either (128 and 64 channels):
 __host__ __device__ constexpr int rows_blocks(int D, int NT, bool ahead) { return NT > 1 ? 2 : ahead ? 3 : D == 64 ? 5 : 4; }
 
-template <int D, int NT, bool AHEAD>
+template <int D, int NT, bool AHEAD, PForm P>
 __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_rows_kernel(const AttnParams p)
 {
     constexpr int ROWS = COLS * NT;
@@ -325,7 +354,7 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
         // query 8 t + r: a quarter of its channels in each of four lanes
         uint2 w[D / 16];
         uint32_t top = 0;
-        const int q = q0 + 8 * t + r;
+        const int q = q0 + 8 * t + (P == P_COLUMNS ? r & 3 : r);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             w[i] = make_uint2(0, 0);
@@ -365,9 +394,9 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
         if (AHEAD && ahead < end)
             load_group(next, p, at, bh, ahead, end);
         if (__any_sync(0xFFFFFFFFu, lane >= 16 && !(now.scale <= 128.f)))
-            group_step<D, NT, true>(st, now, key, end);
+            group_step<D, NT, P, true>(st, now, key, end);
         else
-            group_step<D, NT, false>(st, now, key, end);
+            group_step<D, NT, P, false>(st, now, key, end);
         if (!AHEAD && ahead < end)
             load_group(next, p, at, bh, ahead, end);
         key = ahead;
@@ -411,7 +440,7 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
         for (int w = 0; w < WARPS; ++w) {
             const float f = sm_m[w][row] == -INFINITY ? 1.f : exp2_fast(sm_m[w][row] - m);  // 1: its sums are 0 or NaN
             l += sm_l[w][row] * f;
-            o += sm_o[w][row][ch] * f;
+            o += (P == P_COLUMNS ? sm_o[w][row][ch] + sm_o[w][row + 4][ch] : sm_o[w][row][ch]) * f;
         }
         const long long row_at = bh * p.nq + q;
         if (p.splits > 1) {
@@ -424,6 +453,23 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
                 p.lse[row_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
         }
     }
+}
+
+using RowsKernel = void (*)(const AttnParams);
+template <int D>
+RowsKernel rows_kernel(bool one, bool ahead, PForm form)
+{
+    if (!one)
+        return form == P_PAIR ? cache8_rows_kernel<D, 2, true, P_PAIR> : cache8_rows_kernel<D, 2, true, P_BF16>;
+    if (form == P_COLUMNS)
+        return ahead ? cache8_rows_kernel<D, 1, true, P_COLUMNS> : cache8_rows_kernel<D, 1, false, P_COLUMNS>;
+    if (form == P_PAIR)
+        return ahead ? cache8_rows_kernel<D, 1, true, P_PAIR> : cache8_rows_kernel<D, 1, false, P_PAIR>;
+    return ahead ? cache8_rows_kernel<D, 1, true, P_BF16> : cache8_rows_kernel<D, 1, false, P_BF16>;
+}
+RowsKernel rows_kernel(int d, bool one, bool ahead, PForm form)
+{
+    return d == 64 ? rows_kernel<64>(one, ahead, form) : rows_kernel<128>(one, ahead, form);
 }
 
 // Joins the splits of a query: one warp each.
@@ -641,6 +687,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     if (st != RA_OK)
         return st;
     const Plan pl = plan_of(B, H, d, nq, held * s);
+    const bool pair = split_p(held * s);
     const long long rows = static_cast<long long>(B) * H * nq;
     AttnParams p;
     std::memset(&p, 0, sizeof p);
@@ -670,7 +717,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (pl.many) {
         p.timeout_ns = wait_timeout_ns();
-        if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, pl.one, cs)) != RA_OK)
+        if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, pl.one, pair, cs)) != RA_OK)
             return st;
     } else {
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
@@ -679,12 +726,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
         // warps (eight caches of up to 32768 keys: 179 us, with it 189).  Sixteen queries
         // need the registers for two groups either way (250 us; one group and 12 warps 273).
         const bool one = nq <= COLS, ahead = static_cast<long long>(grid.x) * H * B <= 2 * ONE_WAVE;
-        auto kernel = d == 64 ? (!one ? cache8_rows_kernel<64, 2, true>
-                                 : ahead ? cache8_rows_kernel<64, 1, true>
-                                         : cache8_rows_kernel<64, 1, false>)
-                              : (!one ? cache8_rows_kernel<128, 2, true>
-                                 : ahead ? cache8_rows_kernel<128, 1, true>
-                                         : cache8_rows_kernel<128, 1, false>);
+        auto kernel = rows_kernel(d, one, ahead, nq <= COLS / 2 ? P_COLUMNS : pair ? P_PAIR : P_BF16);
         kernel<<<grid, WARPS * 32, 0, cs>>>(p);
         RA_CUDA_TRY(cudaGetLastError());
     }

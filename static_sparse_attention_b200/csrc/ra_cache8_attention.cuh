@@ -47,8 +47,8 @@ __device__ __forceinline__ long long scale_index(const AttnParams& p, long long 
     return (bh * p.W + slot) * p.blocks + at / CACHE8_BLOCK;
 }
 
-// The many-query kernel (256 queries a block, or 128 if `one`), writing O and lse, or
-// partial results when p.splits > 1.
-ra_status cache8_tiles(const AttnParams& p, int B, int d, bool one, cudaStream_t cs);
+// The many-query kernel (256 queries a block, or 128 if `one`; P as a pair of bf16
+// numbers if `pair`), writing O and lse, or partial results when p.splits > 1.
+ra_status cache8_tiles(const AttnParams& p, int B, int d, bool one, bool pair, cudaStream_t cs);
 
 }  // namespace ra

@@ -61,6 +61,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "ra_cache8_attention.cuh"
 #include "ra_internal.h"
@@ -176,10 +177,10 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 }
 
 // p = 2^(s * c - m) of 32 columns, packed to bf16, summed into four pairs of
-// accumulators; MAX also tracks the largest s.
-template <bool MAX>
+// accumulators; MAX also tracks the largest s, PAIR also returns what the rounding leaves.
+template <bool MAX, bool PAIR>
 __device__ __forceinline__ void exp_columns(const uint32_t (&s)[32], float c, float negm, uint64_t (&sum)[4],
-                                            float (&top)[4], uint32_t (&p)[16])
+                                            float (&top)[4], uint32_t (&p)[16], uint32_t (&rest)[16])
 {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -191,6 +192,9 @@ __device__ __forceinline__ void exp_columns(const uint32_t (&s)[32], float c, fl
         const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
         sum[(e >> 1) & 3] = pair_add(sum[(e >> 1) & 3], pair(p0, p1));
         p[e >> 1] = pack_bf16(p0, p1);
+        if (PAIR)
+            rest[e >> 1] = pack_bf16(p0 - __uint_as_float(p[e >> 1] << 16),
+                                     p1 - __uint_as_float(p[e >> 1] & 0xFFFF0000u));
     }
 }
 
@@ -278,7 +282,10 @@ __device__ __forceinline__ void take_registers()
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-template <int D, bool ONE>
+// PAIR: P is kept as a pair of bf16 numbers, P = hi + lo to 2^-16 of a weight, and P V
+// runs as two products (S is 64 fp32 columns, hi and lo 32 each).  1560 queries, 3120
+// keys, 40 heads of 128: 150 us, with P as one number 128.
+template <int D, bool ONE, bool PAIR>
 __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnParams p)
 {
     using L = Layout<D, ONE>;
@@ -411,6 +418,12 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                 for (int kk = 0; kk < STEP / 16; ++kk)
                     mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + kk * 8, desc_add(vd, kk * 2048), idesc_pv,
                            (i > 0 || kk > 0) ? 1u : 0u);
+                if (PAIR) {
+#pragma unroll
+                    for (int kk = 0; kk < STEP / 16; ++kk)
+                        mma_ts(leader, tmem + o_col(t), tmem + s_col(t, buf) + STEP / 2 + kk * 8,
+                               desc_add(vd, kk * 2048), idesc_pv, 1u);
+                }
                 if (leader) {
                     mma_commit(bar(B_PV_DONE + t));
                     mma_commit(bar(B_V_EMPTY + st));
@@ -567,12 +580,14 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t pk[16];
+                    uint32_t pk[16], rest[16];
                     if (with_max)
-                        exp_columns<true>(s[k], c, -m_use, sum, mx, pk);
+                        exp_columns<true, PAIR>(s[k], c, -m_use, sum, mx, pk, rest);
                     else
-                        exp_columns<false>(s[k], c, -m_use, sum, mx, pk);
+                        exp_columns<false, PAIR>(s[k], c, -m_use, sum, mx, pk, rest);
                     tmem_st16(lanes + col + k * 16, pk);
+                    if (PAIR)
+                        tmem_st16(lanes + col + STEP / 2 + k * 16, rest);
                 }
                 top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 float lo, hi;
@@ -741,7 +756,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
     }
 }
 
-template <int D, bool ONE>
+template <int D, bool ONE, bool PAIR>
 ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
 {
     // the attribute belongs to the function on one device
@@ -750,23 +765,29 @@ ra_status launch(const AttnParams& p, int B, cudaStream_t cs)
     RA_CUDA_TRY(cudaGetDevice(&dev));
     const unsigned long long bit = 1ull << (dev & 63);
     if (dev >= 64 || !(set.load(std::memory_order_acquire) & bit)) {
-        RA_CUDA_TRY(cudaFuncSetAttribute(cache8_tiles_kernel<D, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        RA_CUDA_TRY(cudaFuncSetAttribute(cache8_tiles_kernel<D, ONE, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Layout<D, ONE>::SMEM));
         if (dev < 64)
             set.fetch_or(bit, std::memory_order_release);
     }
     const dim3 grid(static_cast<unsigned>(p.q_tiles) * p.splits, p.H, B);
-    cache8_tiles_kernel<D, ONE><<<grid, THREADS, Layout<D, ONE>::SMEM, cs>>>(p);
+    cache8_tiles_kernel<D, ONE, PAIR><<<grid, THREADS, Layout<D, ONE>::SMEM, cs>>>(p);
     return cuda_fail(cudaGetLastError(), "cache8_tiles_kernel launch");
 }
 
 }  // namespace
 
-ra_status cache8_tiles(const AttnParams& p, int B, int d, bool one, cudaStream_t cs)
+ra_status cache8_tiles(const AttnParams& p, int B, int d, bool one, bool pair, cudaStream_t cs)
 {
-    if (one)
-        return d == 64 ? launch<64, true>(p, B, cs) : launch<128, true>(p, B, cs);
-    return d == 64 ? launch<64, false>(p, B, cs) : launch<128, false>(p, B, cs);
+    auto run = [&](auto D, auto ONE) {
+        return pair ? launch<D(), ONE(), true>(p, B, cs) : launch<D(), ONE(), false>(p, B, cs);
+    };
+    using std::integral_constant;
+    using One = std::true_type;
+    using Two = std::false_type;
+    if (d == 64)
+        return one ? run(integral_constant<int, 64>{}, One{}) : run(integral_constant<int, 64>{}, Two{});
+    return one ? run(integral_constant<int, 128>{}, One{}) : run(integral_constant<int, 128>{}, Two{});
 }
 
 }  // namespace ra

@@ -83,6 +83,9 @@ inline long long extent(long long sb, long long sn, long long sh, int B, int n, 
     return ((B - 1) * sb + (n - 1) * sn + (H - 1) * sh + d) * 2;
 }
 
+// Whether a call over that many keys a query holds P as a hi + lo pair (ra_set_pv_precision).
+bool split_p(long long keys);
+
 struct RopeArgs;
 
 // Launch a kernel that reads what the kernel before it on the stream has written,
