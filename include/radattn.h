@@ -280,10 +280,12 @@ void ra_swc_cache_free(ra_swc_cache* c);
  * ra_qk_norm_rope -- for every row x of q, and of k unless NULL (its number of
  *   heads may differ):
  *     y = R(position) (x * weight / sqrt(mean(x^2) + eps)),
- *   computed in fp32 and rounded once, written to q_out, k_out: bf16
+ *   computed in fp32 and rounded once (a row whose sum of squares leaves fp32's range,
+ *   2^128, is normed by infinity: zeros), written to q_out, k_out: bf16
  *   [B, heads, n, d], contiguous, 16-byte aligned, aliasing nothing else of the
  *   call.  A tensor without a weight is only rotated; rope NULL: no rotation (one
- *   of the two is needed).  eps > 0.  n = 0 is allowed.
+ *   of the two is needed).  Channels that are not rotated do not meet the channel
+ *   beside them, whatever it holds.  eps > 0.  n = 0 is allowed.
  * ra_qk_norm_rope_bwd -- the gradient of that call, given the gradients dy of its
  *   outputs (bf16 [B, heads, n, d], contiguous): dx by its own strides (bf16
  *   [B, n, heads, d]; no two rows may overlap; dq and dk may be slots of one packed

@@ -85,6 +85,24 @@ __device__ __forceinline__ float row_sum(float v)
     return v;
 }
 
+// How many of the lane's four pairs are turned.
+__device__ __forceinline__ int turned_pairs(const RopeArgs& a, int lane_in_row)
+{
+    return a.t_pairs + a.h_pairs + a.w_pairs - 4 * lane_in_row;
+}
+
+// Pairs that are not turned (their angles are 1, 0) are left alone, not multiplied
+// through: an infinity or a NaN would reach the channel beside it.
+__device__ __forceinline__ void keep_unturned(const float (&before)[8], int turned, float (&x)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j >= turned) {
+            x[2 * j] = before[2 * j];
+            x[2 * j + 1] = before[2 * j + 1];
+        }
+}
+
 __device__ __forceinline__ void rotate(const float2 (&cs)[4], float (&x)[8])
 {
 #pragma unroll

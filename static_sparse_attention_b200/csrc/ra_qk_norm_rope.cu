@@ -63,7 +63,29 @@ struct Params {
     float eps;
 };
 
-template <int D>
+// Which of a row's channel pairs are rotated: an instance each, since the third costs
+// registers (108000 tokens, 24 heads of 128 take 48 a thread with all pairs turned, 58
+// with a choice in the loop: one block an SM less).
+enum class Turn { NONE, ALL, SOME };
+
+// Turns a lane's eight channels; in the third form those of its first `turned` pairs.
+template <Turn T, typename Rotate>
+__device__ __forceinline__ void turn_pairs(Rotate&& rotate_by, int turned, float (&x)[8])
+{
+    if (T == Turn::NONE)
+        return;
+    float before[8];
+    if (T == Turn::SOME) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            before[j] = x[j];
+    }
+    rotate_by(x);
+    if (T == Turn::SOME)
+        keep_unturned(before, turned, x);
+}
+
+template <int D, Turn T>
 __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
 {
     constexpr int LPR = D / 8, TOKENS = THREADS / LPR;
@@ -76,11 +98,12 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
     const int i = static_cast<int>(blockIdx.x) * TOKENS + static_cast<int>(threadIdx.x) / LPR;
     const bool live = i < p.n;
     const bool norm = t.weight != nullptr;
+    const int turned = turned_pairs(p.rope, sub);
     float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
     if (norm)
         load_weight(t.weight, t.weight_fp32, sub, w);
     float2 cs[4] = {{1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}};
-    if (p.rope.t && live)
+    if (T != Turn::NONE && live)
         load_rope(p.rope, i, sub, cs);
     const __nv_bfloat16* x = t.x + b * t.sb + (live ? i : 0) * t.sn + sub * 8;
     __nv_bfloat16* y = t.y + (static_cast<long long>(b) * t.H * p.n + (live ? i : 0)) * D + sub * 8;
@@ -100,14 +123,14 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
             unpack_bf16x8(v[u], f);
             if (norm)
                 rms_norm<D>(f, w, p.eps);
-            rotate(cs, f);
+            turn_pairs<T>([&](float (&u)[8]) { rotate(cs, u); }, turned, f);
             if (live)
                 *reinterpret_cast<uint4*>(y + static_cast<long long>(h + u) * p.n * D) = pack_bf16x8(f);
         }
     }
 }
 
-template <int D>
+template <int D, Turn T>
 __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_kernel(const Params p)
 {
     constexpr int LPR = D / 8, TOKENS = THREADS / LPR;
@@ -117,6 +140,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
     const int sub = threadIdx.x % LPR;
     const int tok = static_cast<int>(threadIdx.x) / LPR;
     const bool norm = t.weight != nullptr;
+    const int turned = turned_pairs(p.rope, sub);
     float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f}, dw[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (norm)
         load_weight(t.weight, t.weight_fp32, sub, w);
@@ -130,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
         const int i = tile * TOKENS + tok;
         const bool live = i < p.n;
         float2 cs[4] = {{1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}, {1.f, 0.f}};
-        if (p.rope.t && live)
+        if (T != Turn::NONE && live)
             load_rope(p.rope, i, sub, cs);
         const long long row = live ? i : 0;
         const __nv_bfloat16* x = t.x + b * t.sb + row * t.sn + sub * 8;
@@ -153,7 +177,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
                     break;
                 float g[8];
                 unpack_bf16x8(vg[u], g);
-                rotate_back(cs, g);
+                turn_pairs<T>([&](float (&u)[8]) { rotate_back(cs, u); }, turned, g);
                 if (norm) {
                     float f[8], ss = 0.f, ax = 0.f;
                     unpack_bf16x8(vx[u], f);
@@ -438,6 +462,29 @@ ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, i
     return RA_OK;
 }
 
+using Kernel = void (*)(const Params);
+template <int D>
+Turn turn_of(const RopeArgs& r)
+{
+    return !r.t ? Turn::NONE : r.t_pairs + r.h_pairs + r.w_pairs == D / 2 ? Turn::ALL : Turn::SOME;
+}
+template <int D>
+Kernel forward_kernel(const RopeArgs& r)
+{
+    const Turn t = turn_of<D>(r);
+    return t == Turn::NONE  ? qk_norm_rope_kernel<D, Turn::NONE>
+           : t == Turn::ALL ? qk_norm_rope_kernel<D, Turn::ALL>
+                            : qk_norm_rope_kernel<D, Turn::SOME>;
+}
+template <int D>
+Kernel backward_kernel(const RopeArgs& r)
+{
+    const Turn t = turn_of<D>(r);
+    return t == Turn::NONE  ? qk_norm_rope_bwd_kernel<D, Turn::NONE>
+           : t == Turn::ALL ? qk_norm_rope_bwd_kernel<D, Turn::ALL>
+                            : qk_norm_rope_bwd_kernel<D, Turn::SOME>;
+}
+
 }  // namespace
 }  // namespace ra
 
@@ -493,10 +540,8 @@ extern "C" ra_status ra_qk_norm_rope(const ra_head_rows* q, const ra_head_rows* 
         return fail(RA_ERR_INVALID_ARG, "an output may not alias another buffer of the call");
     const dim3 grid(p.tiles, p.t[0].chunks + p.t[1].chunks, B);
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (d == 64)
-        qk_norm_rope_kernel<64><<<grid, THREADS, 0, cs>>>(p);
-    else
-        qk_norm_rope_kernel<128><<<grid, THREADS, 0, cs>>>(p);
+    auto kernel = d == 64 ? forward_kernel<64>(p.rope) : forward_kernel<128>(p.rope);
+    kernel<<<grid, THREADS, 0, cs>>>(p);
     return cuda_fail(cudaGetLastError(), "qk_norm_rope_kernel launch");
 }
 
@@ -591,10 +636,8 @@ extern "C" ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_ro
     }
     const int blocks = static_cast<int>(items < BWD_BLOCKS ? items : BWD_BLOCKS);
     const dim3 grid(blocks, k ? 2 : 1);
-    if (d == 64)
-        qk_norm_rope_bwd_kernel<64><<<grid, THREADS, 0, cs>>>(p);
-    else
-        qk_norm_rope_bwd_kernel<128><<<grid, THREADS, 0, cs>>>(p);
+    auto kernel = d == 64 ? backward_kernel<64>(p.rope) : backward_kernel<128>(p.rope);
+    kernel<<<grid, THREADS, 0, cs>>>(p);
     RA_CUDA_TRY(cudaGetLastError());
     if (!weights)
         return RA_OK;
