@@ -368,6 +368,11 @@ ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_rows* k, cons
  * ra_cache8_attention_check -- whether ra_cache8_attention would take these
  *   arguments; launches nothing.  For a caller that appends a frame first and must
  *   not find the attention refused behind it.
+ * ra_cache8_attention_plan -- which kernel a call of those sizes runs, and over how
+ *   many ranges of keys that a second launch joins (1: none).  Host only; for tests,
+ *   which name the kernel that they mean, and for tuning.  The kernels of few queries
+ *   take a group of keys at a time or load a second one ahead; the tensor-memory
+ *   kernel has one or two tiles of 128 queries a block.
  * No output may alias another buffer of the call.  Deterministic (no atomics);
  * asynchronous on `stream`; no allocation, so the calls may be captured into a CUDA
  * graph (which replays them with the same frame and held).
@@ -381,6 +386,9 @@ ra_status ra_cache8_attention(const void* Q, const void* k8, const void* v8, con
                               const float* v_scale, void* O, int B, int H, int d, int nq, int s, int window_frames,
                               int held, const int* key_counts, float scale, float* lse, void* workspace,
                               size_t workspace_bytes, ra_stream stream);
+enum { RA_CACHE8_ROWS = 0, RA_CACHE8_ROWS_AHEAD = 1, RA_CACHE8_ONE_TILE = 2, RA_CACHE8_TWO_TILES = 3 };
+ra_status ra_cache8_attention_plan(int B, int H, int d, int nq, int s, int window_frames, int held, int* kernel,
+                                   int* ranges);
 ra_status ra_cache8_attention_check(const void* Q, const void* k8, const void* v8, const float* k_scale,
                                     const float* v_scale, const void* O, int B, int H, int d, int nq, int s,
                                     int window_frames, int held, const int* key_counts, float scale, const float* lse,

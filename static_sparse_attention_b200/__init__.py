@@ -45,6 +45,7 @@ RA_TILE_PARTIAL, RA_TILE_FULL = 0, 1
  RA_ERR_DEVICE_BOUNDS) = range(7)
 RA_TILE = 128
 RA_PV_AUTO, RA_PV_BF16, RA_PV_SPLIT = 0, 1, 2
+RA_CACHE8_ROWS, RA_CACHE8_ROWS_AHEAD, RA_CACHE8_ONE_TILE, RA_CACHE8_TWO_TILES = range(4)
 FAMILIES = {"dense": RA_MASK_DENSE, "radial": RA_MASK_RADIAL, "window3d": RA_MASK_WINDOW3D, "swc": RA_MASK_SWC}
 MODES = {"token_exact": RA_MODE_TOKEN_EXACT, "block": RA_MODE_BLOCK}
 
@@ -107,6 +108,7 @@ _SIGS = {
     "ra_cache8_attention_workspace_bytes": ([_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(ctypes.c_size_t)], _i),
     "ra_cache8_attention": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
                              ctypes.c_size_t, _vp], _i),
+    "ra_cache8_attention_plan": ([_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_i), ctypes.POINTER(_i)], _i),
     "ra_cache8_attention_check": ([_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _f, _vp, _vp,
                                    ctypes.c_size_t], _i),
     "ra_get_device_status": ([_vp], _i),

@@ -549,6 +549,7 @@ constexpr double JOIN_US = 5, JOIN_BYTES_PER_US = 5e6;
 
 struct Plan {
     bool many, one;
+    bool ahead;  // few-query kernel: see AHEAD
     int q_tiles, splits, chunk;
     size_t bytes;
 };
@@ -557,7 +558,7 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
 {
     Plan pl;
     pl.many = nq > 2 * COLS && !(nk <= WHOLE && static_cast<long long>((nq + 2 * COLS - 1) / (2 * COLS)) * H * B <= FEW_BLOCKS);
-    pl.one = false;
+    pl.one = pl.ahead = false;
     const int unit = pl.many ? 64 : GROUP * WARPS;
     long long splits = 1;
     if (pl.many) {
@@ -599,6 +600,11 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
     pl.chunk = pl.chunk < unit ? unit : pl.chunk;
     pl.splits = static_cast<int>((static_cast<long long>(nk) + pl.chunk - 1) / pl.chunk);
     pl.splits = pl.splits < 1 ? 1 : pl.splits;
+    // One wave of blocks waits for its loads: the second group hides them (12480 keys, 24
+    // heads of 128: 25 us, without it 27-29).  Several waves want more warps (eight caches
+    // of up to 32768 keys: 179 us, with it 189).  Sixteen queries need the registers for
+    // two groups either way (250 us; one group and 12 warps 273).
+    pl.ahead = nq > COLS || static_cast<long long>(pl.q_tiles) * pl.splits * H * B <= 2 * ONE_WAVE;
     pl.bytes = pl.splits == 1 ? 0 : static_cast<size_t>(B) * H * nq * pl.splits * (d + 2) * sizeof(float);
     return pl;
 }
@@ -637,6 +643,20 @@ extern "C" ra_status ra_cache8_attention_workspace_bytes(int B, int H, int d, in
     if (st == RA_OK)
         *bytes = plan_of(B, H, d, nq, held * s).bytes;
     return st;
+}
+
+extern "C" ra_status ra_cache8_attention_plan(int B, int H, int d, int nq, int s, int window_frames, int held,
+                                              int* kernel, int* ranges)
+{
+    const ra_status st = check_attention(B, H, d, nq, s, window_frames, held);
+    if (st != RA_OK)
+        return st;
+    if (!kernel || !ranges)
+        return fail(RA_ERR_INVALID_ARG, "NULL output pointer");
+    const Plan pl = plan_of(B, H, d, nq, held * s);
+    *kernel = pl.many ? (pl.one ? RA_CACHE8_ONE_TILE : RA_CACHE8_TWO_TILES) : (pl.ahead ? RA_CACHE8_ROWS_AHEAD : RA_CACHE8_ROWS);
+    *ranges = pl.splits;
+    return RA_OK;
 }
 
 extern "C" ra_status ra_cache8_attention_check(const void* Q, const void* k8, const void* v8, const float* k_scale,
@@ -721,12 +741,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
             return st;
     } else {
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
-        // One wave of blocks waits for its loads: the second group hides them (12480
-        // keys, 24 heads of 128: 25 us, without it 27-29).  Several waves want more
-        // warps (eight caches of up to 32768 keys: 179 us, with it 189).  Sixteen queries
-        // need the registers for two groups either way (250 us; one group and 12 warps 273).
-        const bool one = nq <= COLS, ahead = static_cast<long long>(grid.x) * H * B <= 2 * ONE_WAVE;
-        auto kernel = rows_kernel(d, one, ahead, nq <= COLS / 2 ? P_COLUMNS : pair ? P_PAIR : P_BF16);
+        auto kernel = rows_kernel(d, nq <= COLS, pl.ahead, nq <= COLS / 2 ? P_COLUMNS : pair ? P_PAIR : P_BF16);
         kernel<<<grid, WARPS * 32, 0, cs>>>(p);
         RA_CUDA_TRY(cudaGetLastError());
     }
