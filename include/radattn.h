@@ -36,9 +36,9 @@
  *   - A kernel that gives up a bounded internal wait records
  *     RA_ERR_DEVICE_TIMEOUT in a per-device error word; ra_get_device_status
  *     reads (and clears) it.  Kernels never trap.  The word is sticky: while it
- *     is set, every later forward, backward or SWC-step kernel and every attention
- *     over the 8-bit ring of more than 16 queries on that device
- *     does no work and leaves its outputs unwritten, although its entry point
+ *     is set, every later forward, backward or SWC-step kernel, and of the attention
+ *     over the 8-bit ring the tensor-memory kernel (see ra_cache8_attention_plan), on
+ *     that device does no work and leaves its outputs unwritten, although its entry point
  *     returned RA_OK when it was enqueued.  Check ra_get_device_status before
  *     trusting outputs produced after a possible timeout; it clears the word.
  *   - Results are deterministic: the same inputs give the same bits.

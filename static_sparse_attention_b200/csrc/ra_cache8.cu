@@ -48,6 +48,8 @@ struct AppendParams {
     int groups, heads;          // groups of heads, heads of a group
     RopeArgs rope;
     float eps;
+    long long x_size[2], code_size, scale_size;  // elements that x spans, of a ring, of its scales
+    int* err;                   // debug build: see ra_bounds.cuh
 };
 
 // The larger magnitude; NaN if one is.
@@ -88,7 +90,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& s
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             v[i] = make_uint4(0, 0, 0, 0);
-            if (in(i))
+            if (in(i) && inside(p.err, x + i * row_step - p.x[WHICH], 8, p.x_size[WHICH], SITE_I_IN))
                 v[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * row_step));
         }
         x += p.sh[WHICH];
@@ -170,7 +172,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& s
         const bool finite = bits < 0x7F800000u;
         int k = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
         k = bits == 0 || !finite ? 0 : max(k, -126);
-        if (threadIdx.x == 0)
+        if (threadIdx.x == 0 && inside(p.err, (head * p.W + slot) * p.blocks + blk, 1, p.scale_size, SITE_I_SCALE))
             p.scale[WHICH][(head * p.W + slot) * p.blocks + blk] =
                 __uint_as_float(finite ? static_cast<uint32_t>(k + 127) << 23 : 0x7FFFFFFFu);
         // 1 / scale, in two factors where r * (1 / scale) would overflow
@@ -195,7 +197,7 @@ __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& s
             uint2 word = make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
             if (!finite)
                 word = make_uint2(0, 0);
-            if (in(i))
+            if (in(i) && inside(p.err, code + static_cast<long long>(i) * step * D - p.code[WHICH], 8, p.code_size, SITE_I_CODE))
                 *reinterpret_cast<uint2*>(code + static_cast<size_t>(i) * step * D) = word;
         }
         ++head;
@@ -321,6 +323,12 @@ extern "C" ra_status ra_cache8_append(const ra_head_rows* k, const ra_head_rows*
     p.slot0 = static_cast<int>(frame % W);
     p.eps = eps;
     const long long heads = static_cast<long long>(B) * H;
+    p.code_size = heads * W * s * d;
+    p.scale_size = heads * W * p.blocks;
+    for (int i = 0; i < 2; ++i)
+        p.x_size[i] = extent(p.sb[i], p.sn[i], p.sh[i], B, n, H, d) / 2;
+    if ((st = bounds_word(&p.err)) != RA_OK)
+        return st;
     const Span out[4] = {span(k8, heads * W * s * d), span(v8, heads * W * s * d),
                          span(k_scale, heads * W * p.blocks * 4), span(v_scale, heads * W * p.blocks * 4)};
     const Span in[3] = {span(k->x, extent(p.sb[0], p.sn[0], p.sh[0], B, n, H, d)),

@@ -124,7 +124,8 @@ __device__ __forceinline__ Places places_of(const AttnParams& p, long long bh)
 }
 
 template <int D, bool WHOLE_GROUP>
-__device__ __forceinline__ void load_codes(Group<D>& g, const Places& at, int key0, int end)
+__device__ __forceinline__ void load_codes(Group<D>& g, const AttnParams& p, const Places& at, long long bh, int key0,
+                                           int end)
 {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const uint8_t *k = at.k + static_cast<long long>(key0) * D, *v = at.v + static_cast<long long>(key0) * D;
@@ -134,7 +135,7 @@ __device__ __forceinline__ void load_codes(Group<D>& g, const Places& at, int ke
         for (int i = 0; i < Group<D>::KP; ++i) {
             if (!WHOLE_GROUP)
                 g.k[t][i] = make_uint4(0, 0, 0, 0);
-            if (WHOLE_GROUP || key0 + 8 * t + r < end)
+            if ((WHOLE_GROUP || key0 + 8 * t + r < end) && keys_inside(p, bh, key0 + 8 * t + r, 1))
                 g.k[t][i] = __ldcs(reinterpret_cast<const uint4*>(k + 8 * t * D + 64 * i));
         }
     }
@@ -146,7 +147,7 @@ __device__ __forceinline__ void load_codes(Group<D>& g, const Places& at, int ke
             for (int i = 0; i < Group<D>::VW; ++i)
                 g.v[t][i] = 0;
         }
-        if (WHOLE_GROUP || key0 + 2 * c + row < end) {
+        if ((WHOLE_GROUP || key0 + 2 * c + row < end) && keys_inside(p, bh, key0 + 2 * c + row, 1)) {
             if (D == 128) {
                 const uint4 w = __ldcs(reinterpret_cast<const uint4*>(v + row * D));
                 g.v[t][0] = w.x, g.v[t][1] = w.y, g.v[t][Group<D>::VW - 2] = w.z, g.v[t][Group<D>::VW - 1] = w.w;
@@ -163,7 +164,7 @@ template <int D>
 __device__ __forceinline__ void prefetch_group(const AttnParams& p, const Places& at, long long bh, int key0, int end)
 {
     const int key = key0 + static_cast<int>(threadIdx.x & 15);
-    if (key < end) {
+    if (key < end && keys_inside(p, bh, key, 1) && scale_inside(p, scale_index(p, bh, key))) {
         asm volatile("prefetch.global.L2 [%0];" ::"l"(at.ahead + static_cast<long long>(key0) * D));
         asm volatile("prefetch.global.L2 [%0];" ::"l"(at.scale + scale_index(p, bh, key)));
     }
@@ -176,11 +177,11 @@ __device__ __forceinline__ void load_group(Group<D>& g, const AttnParams& p, con
                                            int end)
 {
     if (key0 + GROUP <= end)
-        load_codes<D, true>(g, at, key0, end);
+        load_codes<D, true>(g, p, at, bh, key0, end);
     else
-        load_codes<D, false>(g, at, key0, end);
+        load_codes<D, false>(g, p, at, bh, key0, end);
     const int key = key0 + static_cast<int>(threadIdx.x & 15);
-    g.scale = key < end ? at.scale[scale_index(p, bh, key)] : 0.f;
+    g.scale = key < end && scale_inside(p, scale_index(p, bh, key)) ? at.scale[scale_index(p, bh, key)] : 0.f;
     prefetch_group<D>(p, at, bh, key0 + PREFETCH * WARPS * GROUP, end);
 }
 
@@ -358,7 +359,7 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             w[i] = make_uint2(0, 0);
-            if (q < p.nq)
+            if (q < p.nq && row_inside(p, bh * p.nq + q, SITE_I_QUERY))
                 w[i] = *reinterpret_cast<const uint2*>(p.Q + (bh * p.nq + q) * D + 64 * (i / 4) + 16 * c + 4 * (i % 4));
             top = max(top, max(max(w[i].x & 0x7FFFu, (w[i].x >> 16) & 0x7FFFu),
                                max(w[i].y & 0x7FFFu, (w[i].y >> 16) & 0x7FFFu)));
@@ -443,6 +444,8 @@ __global__ void __launch_bounds__(WARPS * 32, rows_blocks(D, NT, AHEAD)) cache8_
             o += (P == P_COLUMNS ? sm_o[w][row][ch] + sm_o[w][row + 4][ch] : sm_o[w][row][ch]) * f;
         }
         const long long row_at = bh * p.nq + q;
+        if (!row_inside(p, row_at, SITE_I_RESULT) || (p.splits > 1 && !part_inside(p, row_at * p.splits + split)))
+            break;
         if (p.splits > 1) {
             p.part_o[(row_at * p.splits + split) * D + ch] = o;
             if (ch == 0)
@@ -477,7 +480,7 @@ template <int D>
 __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, long long rows)
 {
     wait_for_previous();
-    if (p.err && *reinterpret_cast<volatile int*>(p.err) != 0)
+    if (p.skip_on_error && *reinterpret_cast<volatile int*>(p.err) != 0)
         return;  // a block gave up: the parts are not whole
     const long long at = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -485,6 +488,8 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
         return;
     const int b = static_cast<int>(at / (static_cast<long long>(p.H) * p.nq));
     const int n = (key_count(p, b) + p.chunk - 1) / p.chunk;
+    if (!row_inside(p, at, SITE_I_RESULT) || (n && !part_inside(p, at * p.splits + n - 1)))
+        return;
     const float2* ml = p.part_ml + at * p.splits;
     float m = -INFINITY;
     for (int k = lane; k < n; k += 32)
@@ -719,6 +724,7 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     p.counts = key_counts;
     p.O = static_cast<__nv_bfloat16*>(O);
     p.lse = lse;
+    p.B = B;
     p.H = H;
     p.nq = nq;
     p.s = s;
@@ -737,9 +743,12 @@ extern "C" ra_status ra_cache8_attention(const void* Q, const void* k8, const vo
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (pl.many) {
         p.timeout_ns = wait_timeout_ns();
+        p.skip_on_error = true;
         if ((st = device_error_word(&p.err)) != RA_OK || (st = cache8_tiles(p, B, d, pl.one, pair, cs)) != RA_OK)
             return st;
     } else {
+        if ((st = bounds_word(&p.err)) != RA_OK)
+            return st;
         const dim3 grid(static_cast<unsigned>(pl.q_tiles) * pl.splits, H, B);
         auto kernel = rows_kernel(d, nq <= COLS, pl.ahead, nq <= COLS / 2 ? P_COLUMNS : pair ? P_PAIR : P_BF16);
         kernel<<<grid, WARPS * 32, 0, cs>>>(p);

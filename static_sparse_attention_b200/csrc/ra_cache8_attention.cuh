@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include "ra_bounds.cuh"
 #include "ra_cache8.cuh"
 #include "ra_internal.h"
 
@@ -25,7 +26,9 @@ struct AttnParams {
     uint32_t per_s;          // floor(2^32 / s) (2^32 - 1 for s = 1): see scale_index
     int q_tiles, splits, chunk;  // tiles of queries; ranges of keys, each of `chunk` keys
     float scale_log2;        // scale * log2(e)
-    int* err;                // the library's device error word
+    int B;
+    int* err;                // the library's device error word (few-query kernel: debug build only)
+    bool skip_on_error;      // the kernel before the join may have given up
     unsigned long long timeout_ns;
 };
 
@@ -45,6 +48,26 @@ __device__ __forceinline__ long long scale_index(const AttnParams& p, long long 
         at -= p.s;
     }
     return (bh * p.W + slot) * p.blocks + at / CACHE8_BLOCK;
+}
+
+// Bounds checks of the debug build (see ra_bounds.cuh): `n` keys of head bh from `key`
+// on, their scale's index, a query's row, a partial result's.
+__device__ __forceinline__ bool keys_inside(const AttnParams& p, long long bh, long long key, long long n)
+{
+    return inside(p.err, key, n, p.nk, SITE_I_CODE) &&
+           inside(p.err, bh * p.W * p.s + key, n, static_cast<long long>(p.B) * p.H * p.W * p.s, SITE_I_CODE);
+}
+__device__ __forceinline__ bool scale_inside(const AttnParams& p, long long at)
+{
+    return inside(p.err, at, 1, static_cast<long long>(p.B) * p.H * p.W * p.blocks, SITE_I_SCALE);
+}
+__device__ __forceinline__ bool row_inside(const AttnParams& p, long long row, int site)
+{
+    return inside(p.err, row, 1, static_cast<long long>(p.B) * p.H * p.nq, site);
+}
+__device__ __forceinline__ bool part_inside(const AttnParams& p, long long at)
+{
+    return inside(p.err, at, 1, static_cast<long long>(p.B) * p.H * p.nq * p.splits, SITE_I_PART);
 }
 
 // The many-query kernel (256 queries a block, or 128 if `one`; P as a pair of bf16

@@ -89,7 +89,7 @@ constexpr float RAISE = 8.0f;
 
 enum : int {
     SITE_RAW_EMPTY = 60, SITE_RAW_FULL, SITE_K_EMPTY, SITE_V_EMPTY, SITE_K_FULL, SITE_V_FULL, SITE_P_FULL, SITE_S_FULL,
-    SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN
+    SITE_PV_DONE, SITE_O_FINAL, SITE_SMEM_ALIGN, SITE_B_KEYS
 };
 
 // ONE: a single tile of queries (see Turns).
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
         for (int j = 0; j < LOADS; ++j) {
             const int i = i0 + THREADS * j, row = i / UNITS;
             v[j] = make_uint4(0, 0, 0, 0);
-            if (row < tiles * TILE_ROWS && q0 + row < p.nq)
+            if (row < tiles * TILE_ROWS && q0 + row < p.nq && row_inside(p, bh * p.nq + q0 + row, SITE_I_QUERY))
                 v[j] = *reinterpret_cast<const uint4*>(p.Q + (bh * p.nq + q0 + row) * D + i % UNITS * 8);
         }
 #pragma unroll
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                 for (int i = 0; i < 4; ++i) {
                     const int key = begin + hh * STEP + lane + 32 * (i & 1);
                     scale[i] = 0.f;
-                    if (key < end)
+                    if (key < end && scale_inside(p, scale_index(p, bh, key)))
                         scale[i] = __ldg((i < 2 ? p.k_scale : p.v_scale) + scale_index(p, bh, key));
                 }
             };
@@ -478,8 +478,12 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                     factors[2 * STEP] = two ? 1u : 0u;
                 }
                 __syncwarp();
+                // (debug build: nothing is copied, and the other roles leave their waits)
+                const int keys = min(STEP, end - begin - hh * STEP);
+                if (!in_bounds(wc, keys_inside(p, bh, begin + hh * STEP, keys), SITE_B_KEYS))
+                    break;
                 if (lane == 0) {
-                    const uint32_t bytes = static_cast<uint32_t>(min(STEP, end - begin - hh * STEP)) * D;
+                    const uint32_t bytes = static_cast<uint32_t>(keys) * D;
                     const uint32_t raw = sbase + L::RAW_OFF + rs * 2 * L::RAW_TILE;
                     const long long at = first + static_cast<long long>(hh) * L::RAW_TILE;
                     mbar_arrive_expect_tx(bar(B_RAW_FULL + rs), 2 * bytes);
@@ -724,6 +728,8 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                 }
                 if (!row_valid)
                     continue;
+                if (!row_inside(p, at, SITE_I_RESULT) || (p.splits > 1 && !part_inside(p, at * p.splits + split)))
+                    continue;
                 if (p.splits > 1) {
                     float4* dst = reinterpret_cast<float4*>(p.part_o + (at * p.splits + split) * D + k * 32);
 #pragma unroll
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(THREADS, 1) cache8_tiles_kernel(const AttnPara
                                             pack_bf16(x[8 * u + 6], x[8 * u + 7]));
                 }
             }
-            if (row_valid) {
+            if (row_valid && row_inside(p, at, SITE_I_RESULT)) {
                 if (p.splits > 1)
                     p.part_ml[at * p.splits + split] = make_float2(m_run, l_run);
                 else if (p.lse)

@@ -13,6 +13,8 @@
 
 #include <cstdint>
 
+#include "ra_bounds.cuh"
+
 namespace ra {
 
 // Position tables: fp32 (cos, sin) pairs, [len][pairs][2] for each axis.
@@ -23,6 +25,8 @@ struct RopeArgs {
     int t_pairs, h_pairs, w_pairs;
     int grid_h, grid_w;  // token i of a call: frame first + i / (grid_h * grid_w), row-major within it
     int first;           // frame of the call's first token
+    int frames;          // rows of t
+    int* err;            // debug build: see ra_bounds.cuh
 };
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float (&x)[8])
@@ -71,6 +75,11 @@ __device__ __forceinline__ void load_rope(const RopeArgs& a, int i, int lane_in_
     for (int j = 0; j < 4; ++j) {
         const int p = lane_in_row * 4 + j;
         const float2* at = p < a.t_pairs ? t : (p < a.t_pairs + a.h_pairs ? h : w);
+        if (!inside(a.err, p < a.t_pairs ? a.first + f : p < a.t_pairs + a.h_pairs ? row : col, 1,
+                    p < a.t_pairs ? a.frames : p < a.t_pairs + a.h_pairs ? a.grid_h : a.grid_w, SITE_I_ROPE)) {
+            cs[j] = make_float2(1.f, 0.f);
+            continue;
+        }
         cs[j] = p < a.t_pairs + a.h_pairs + a.w_pairs ? __ldg(at + p) : make_float2(1.f, 0.f);
     }
 }

@@ -53,6 +53,7 @@ struct Rows {
     long long gb, gn, gh;
     float* dw_part;          // backward: [blocks][d], null: no weight
     float* dw;               // [d]
+    long long x_size, y_size, dx_size;  // elements that x, y (and dy) and dx span
 };
 
 struct Params {
@@ -61,6 +62,7 @@ struct Params {
     int n, B, tiles;  // tiles: token tiles of one batch element
     int heads;        // heads per chunk
     float eps;
+    int* err;         // debug build: see ra_bounds.cuh
 };
 
 // Which of a row's channel pairs are rotated: an instance each, since the third costs
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
 #pragma unroll
         for (int u = 0; u < HEADS_IN_FLIGHT; ++u) {
             v[u] = make_uint4(0, 0, 0, 0);
-            if (live && h + u < h1)
+            if (live && h + u < h1 && inside(p.err, x + (h + u) * t.sh - t.x, 8, t.x_size, SITE_I_IN))
                 v[u] = __ldcs(reinterpret_cast<const uint4*>(x + (h + u) * t.sh));
         }
 #pragma unroll
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(THREADS) qk_norm_rope_kernel(const Params p)
             if (norm)
                 rms_norm<D>(f, w, p.eps);
             turn_pairs<T>([&](float (&u)[8]) { rotate(cs, u); }, turned, f);
-            if (live)
+            if (live && inside(p.err, y + static_cast<long long>(h + u) * p.n * D - t.y, 8, t.y_size, SITE_I_OUT))
                 *reinterpret_cast<uint4*>(y + static_cast<long long>(h + u) * p.n * D) = pack_bf16x8(f);
         }
     }
@@ -165,7 +167,9 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
 #pragma unroll
             for (int u = 0; u < HEADS_IN_FLIGHT; ++u) {
                 vx[u] = vg[u] = make_uint4(0, 0, 0, 0);
-                if (live && h + u < h1) {
+                if (live && h + u < h1 &&
+                    inside(p.err, dy + static_cast<long long>(h + u) * p.n * D - t.dy, 8, t.y_size, SITE_I_GRAD_IN) &&
+                    (!norm || inside(p.err, x + (h + u) * t.sh - t.x, 8, t.x_size, SITE_I_IN))) {
                     vg[u] = __ldcs(reinterpret_cast<const uint4*>(dy + static_cast<long long>(h + u) * p.n * D));
                     if (norm)
                         vx[u] = __ldcs(reinterpret_cast<const uint4*>(x + (h + u) * t.sh));
@@ -196,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
                         g[j] = r * fmaf(-f[j], c, g[j] * w[j]);
                     }
                 }
-                if (live)
+                if (live && inside(p.err, dx + (h + u) * t.gh - t.dx, 8, t.dx_size, SITE_I_GRAD_OUT))
                     *reinterpret_cast<uint4*>(dx + (h + u) * t.gh) = pack_bf16x8(g);
             }
         }
@@ -214,7 +218,8 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
 #pragma unroll
         for (int r = 0; r < TOKENS; ++r)
             s += part[r][threadIdx.x];
-        t.dw_part[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
+        if (inside(p.err, static_cast<long long>(blockIdx.x) * D + threadIdx.x, 1, BWD_BLOCKS * D, SITE_I_PART))
+            t.dw_part[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = s;
     }
 }
 
@@ -231,7 +236,8 @@ __global__ void __launch_bounds__(1024) weight_grad_kernel(const Params p, int b
     const int c = threadIdx.x % D, g = threadIdx.x / D;
     float s = 0.f;
     for (int k = g; k < blocks; k += G)
-        s += t.dw_part[static_cast<size_t>(k) * D + c];
+        if (inside(p.err, static_cast<long long>(k) * D + c, 1, BWD_BLOCKS * D, SITE_I_PART))
+            s += t.dw_part[static_cast<size_t>(k) * D + c];
     part[g][c] = s;
     __syncthreads();
     if (g == 0) {
@@ -367,7 +373,8 @@ ra_status rope_args(const ra_rope* rope, int frame0, int n, int d, RopeArgs* out
     out->grid_h = rope->grid_h;
     out->grid_w = rope->grid_w;
     out->first = frame0;
-    return RA_OK;
+    out->frames = rope->frames;
+    return bounds_word(&out->err);
 }
 
 ra_status head_rows_args(const char* what, const ra_head_rows* r, int B, int n, int d, long long* sb, long long* sn,
@@ -452,6 +459,8 @@ ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, i
         t.weight = in[i]->weight;
         t.weight_fp32 = in[i]->weight_fp32;
         t.H = in[i]->heads;
+        t.x_size = extent(t.sb, t.sn, t.sh, B, n, t.H, d) / 2;
+        t.y_size = static_cast<long long>(B) * t.H * n * d;
         H = t.H > H ? t.H : H;
     }
     if (static_cast<long long>(B) * H * n > (1LL << 40))
@@ -459,7 +468,7 @@ ra_status fill(Params* p, const ra_head_rows* q, const ra_head_rows* k, int B, i
     p->heads = heads_per_chunk(p->tiles, B, H, slots, whole_rounds);
     for (int i = 0; i < 2; ++i)
         p->t[i].chunks = (p->t[i].H + p->heads - 1) / p->heads;
-    return RA_OK;
+    return bounds_word(&p->err);
 }
 
 using Kernel = void (*)(const Params);
@@ -590,6 +599,7 @@ extern "C" ra_status ra_qk_norm_rope_bwd(const ra_head_rows* q, const ra_head_ro
         t.dy = static_cast<const __nv_bfloat16*>(g->dy);
         t.dx = static_cast<__nv_bfloat16*>(g->dx);
         t.dw = g->dweight;
+        t.dx_size = extent(t.gb, t.gn, t.gh, B, n, t.H, d) / 2;
         weights |= t.dw != nullptr;
         if (n > 0) {
             outs[n_out++] = span(t.dx, extent(t.gb, t.gn, t.gh, B, n, t.H, d));

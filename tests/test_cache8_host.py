@@ -60,3 +60,18 @@ def test_the_check_refuses_what_the_attention_refuses(ra):
         st = ra.ra_cache8_attention_check(*args.values())
         assert st != ra.RA_OK and ra.ra_last_error(), bad
         assert ra.ra_cache8_attention(*args.values(), None) == st, bad
+
+
+@pytest.mark.parametrize("source,checks", [
+    ("ra_head_rows.cuh", ["SITE_I_ROPE"]),
+    ("ra_qk_norm_rope.cu", ["SITE_I_IN", "SITE_I_OUT", "SITE_I_GRAD_IN", "SITE_I_GRAD_OUT", "SITE_I_PART"]),
+    ("ra_cache8.cu", ["SITE_I_IN", "SITE_I_CODE", "SITE_I_SCALE"]),
+    ("ra_cache8_attention.cu", ["keys_inside", "scale_inside", "row_inside", "part_inside"]),
+    ("ra_cache8_tiles.cu", ["keys_inside", "scale_inside", "row_inside", "part_inside"]),
+])
+def test_the_debug_build_checks_each_buffer_of_the_operators(source, checks):
+    """The debug library's promise, that each global offset is checked before use, for the
+    kernels around the attention: their sources hold one for each buffer."""
+    src = open(os.path.join(CSRC, source)).read()
+    for check in checks:
+        assert check in src, check
