@@ -10,7 +10,8 @@ CPython extension, _torch_binding.so.
 
 There is no CPU fallback: importing this package fails loudly when the
 compiled library is missing (build it with
-`python static_sparse_attention_b200/build.py`).
+`python static_sparse_attention_b200/build.py`), and so does the first call of an
+operator whose extension is; the C entry points need neither it nor torch.
 """
 from __future__ import annotations
 
@@ -31,9 +32,6 @@ LIB_PATH = os.path.join(_PKG, "libradattn_debug.so" if VARIANT == "debug" else "
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{os.path.basename(LIB_PATH)} is not built ({LIB_PATH}); run "
                       f"`python static_sparse_attention_b200/build.py{' --debug' if VARIANT == 'debug' else ''}`")
-
-if not os.path.exists(os.path.join(_PKG, "_torch_binding.so")):
-    raise ImportError("_torch_binding.so is not built; run `python static_sparse_attention_b200/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
 
@@ -415,6 +413,8 @@ def _load_binding():
     if _binding is None:
         import torch  # noqa: F401  (its libraries have to be loaded first)
 
+        if not os.path.exists(os.path.join(_PKG, "_torch_binding.so")):
+            raise ImportError("_torch_binding.so is not built; run `python static_sparse_attention_b200/build.py`")
         from . import _torch_binding as module
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in
                       (ra_qk_norm_rope, ra_qk_norm_rope_bwd_workspace_bytes, ra_qk_norm_rope_bwd, ra_cache8_append,

@@ -9,13 +9,14 @@ they derive from their inputs and record a failure in the device error word
 (RA_ERR_DEVICE_BOUNDS) instead of making the access.  The binding loads it when
 RA_LIBRARY_VARIANT=debug is set.
 
-Both also build _torch_binding.so (g++, torch's headers), the tensor checks of the
-operators whose calls last microseconds; it takes the entry points' addresses from
-the package and is not linked to the library.
+Where torch is installed both also build _torch_binding.so (g++, torch's headers), the
+tensor checks of the operators whose calls last microseconds; it takes the entry points'
+addresses from the package and is not linked to the library, which needs no torch.
 """
 from __future__ import annotations
 
 import glob
+import hashlib
 import importlib.util
 import os
 import subprocess
@@ -61,13 +62,35 @@ def nvcc() -> str:
 
 BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
 BINDING = os.path.join(PKG, "_torch_binding.so")
+BINDING_TORCH = os.path.join(PKG, "_build", "binding_torch")  # which torch it was built for
 
 
-def build_binding(force: bool = False) -> str:
-    deps = (BINDING_SRC, os.path.join(INCLUDE, "radattn.h"))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
+def _torch_folder() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec else None
+
+
+def _torch_version(torch: str) -> str:
+    with open(os.path.join(torch, "version.py")) as fh:
+        return hashlib.sha256(fh.read().encode()).hexdigest()
+
+
+def _binding_stale(torch: str) -> bool:
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_TORCH):
+        return True
+    with open(BINDING_TORCH) as fh:  # the extension fits one torch's headers
+        if fh.read() != _torch_version(torch):
+            return True
+    return any(os.path.getmtime(p) > os.path.getmtime(BINDING) for p in (BINDING_SRC, os.path.join(INCLUDE, "radattn.h")))
+
+
+def build_binding(force: bool = False) -> str | None:
+    """The tensor side of the operators; None without torch (the library needs none)."""
+    torch = _torch_folder()
+    if torch is None:
+        return None
+    if not force and not _binding_stale(torch):
         return BINDING
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
     tmp = BINDING + f".tmp{os.getpid()}"
     # the compiler on PATH, as nvcc's host compiler: one that links its own copy of
@@ -79,13 +102,16 @@ def build_binding(force: bool = False) -> str:
         "-L", os.path.join(torch, "lib"),
         *("-l" + lib for lib in ("torch_python", "torch", "torch_cpu", "torch_cuda", "c10", "c10_cuda"))])
     os.replace(tmp, BINDING)
+    os.makedirs(os.path.dirname(BINDING_TORCH), exist_ok=True)
+    with open(BINDING_TORCH, "w") as fh:
+        fh.write(_torch_version(torch))
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     lib = LIB_DEBUG if debug else LIB
-    build_binding(force)
     if not force and not _stale(lib):
+        build_binding(force)
         return lib
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *NVCC_FLAGS, *(["-DRA_DEBUG_BOUNDS"] if debug else []), "-I", INCLUDE, "-I", CSRC, *sources(),
@@ -94,6 +120,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         cmd[1:1] = ["-Xptxas", "-v"]
     subprocess.check_call(cmd)
     os.replace(tmp, lib)
+    build_binding(force)
     return lib
 
 
