@@ -175,16 +175,20 @@ __device__ __forceinline__ void append_block(const AppendParams& p, Shared<D>& s
         if (threadIdx.x == 0 && inside(p.err, (head * p.W + slot) * p.blocks + blk, 1, p.scale_size, SITE_I_SCALE))
             p.scale[WHICH][(head * p.W + slot) * p.blocks + blk] =
                 __uint_as_float(finite ? static_cast<uint32_t>(k + 127) << 23 : 0x7FFFFFFFu);
-        // 1 / scale, in two factors where r * (1 / scale) would overflow
-        const int k1 = max(k, -100);
+        // 1 / scale, joined to the norm's factor: r is below 2^75 (1 / sqrt of the least eps),
+        // so that r / scale stays finite down to scales of 2^-50, and is taken in three
+        // factors below.
+        const int k1 = max(k, -50);
         const float inverse = __uint_as_float(static_cast<uint32_t>(127 - k1) << 23);
         if (k1 != k) {
             const float rest = __uint_as_float(static_cast<uint32_t>(127 + k1 - k) << 23);
 #pragma unroll
-            for (int i = 0; i < PASSES; ++i)
+            for (int i = 0; i < PASSES; ++i) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    f[i][j] *= rest;
+                    f[i][j] = f[i][j] * r[i] * rest;
+                r[i] = 1.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
