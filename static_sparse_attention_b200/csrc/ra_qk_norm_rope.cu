@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(THREADS, BWD_BLOCKS_PER_SM) qk_norm_rope_bwd_k
                     ss = row_sum<LPR>(ss);
                     ax = row_sum<LPR>(ax);
                     const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                    const float c = r * r * (ax * (1.f / D));  // dx = r * (a - x * c)
+                    const float c = r * (r * (ax * (1.f / D)));  // dx = r * (a - x * c); r^2 alone may overflow
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         dw[j] = fmaf(g[j], f[j] * r, dw[j]);

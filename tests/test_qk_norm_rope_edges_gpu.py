@@ -5,7 +5,7 @@ import math
 import pytest
 import torch
 
-from tests import _gpu
+from tests import _gpu, _heads
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,23 @@ def test_an_infinity_in_a_normed_row(rotated):
     want[33] = NAN
     assert _same(y[0, 1, 2], want)
     assert bool(torch.isfinite(y[0, 0]).all()) and bool(torch.isfinite(y[0, 1, [0, 1, 3]]).all())
+
+
+@pytest.mark.parametrize("eps", [1e-12, 1e-38, 1e-44])
+def test_gradient_of_zero_and_small_rows_with_a_small_eps(eps):
+    """The norm's factor is up to 2^75, its square no fp32 number: rows of zeros have the
+    gradient dy * w / sqrt(eps), small rows the formula's."""
+    _gpu.need_gpu()
+    ra = _gpu.ra()
+    d = 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(1, 6, 2, d, generator=g, device="cuda").bfloat16()
+    x[0, 1] = 0
+    x[0, 2] *= 1e-15
+    w = (1 + 0.3 * torch.randn(d, generator=g, device="cuda")).bfloat16()
+    dy = (torch.randn(1, 2, 6, d, generator=g, device="cuda") * 1e-6).bfloat16()
+    dx, _, dw, _ = ra.qk_norm_rope_bwd(x, None, dy, None, w, eps=eps)
+    eps = torch.tensor(eps, dtype=torch.float32).double().item()  # as the call rounds it
+    want, bound, dw64, dw_bound = _heads.norm_rope_bwd(x, dy, w, None, 0, eps)
+    assert bool(((dx.double().cpu() - want).abs() <= bound).all())
+    assert bool(((dw.double().cpu() - dw64).abs() <= dw_bound).all())
