@@ -8,9 +8,10 @@
 // (K), and kept in registers; the block's largest magnitude fixes the scale, the
 // least power of two that brings it to at most 448, and the codes are rounded once,
 // to nearest even, from fp32.  Bound by memory: 3 bytes a value (2 read, 1 written).
-// 12 frames of 3555 tokens, 24 heads of 128: 156 us, 77 % of the measured copy rate
+// 12 frames of 3555 tokens, 24 heads of 128: 155 us, 77 % of the measured copy rate
 // (120 us); issue slots 58 %, DRAM 59 % busy, the rest is the barrier that fixes a
-// block's scale.  With a thread block for each head the position look-up was a third
+// block's scale.  (80 registers a thread, three blocks an SM of 128 channels, leave 28
+// bytes of spills.)  With a thread block for each head the position look-up was a third
 // of the instructions: 247 us.
 //
 // The scale's power of two costs no precision against amax / 448: e4m3 is a
@@ -32,9 +33,11 @@ namespace {
 
 constexpr int PASSES = 4;         // row groups of a block held in registers
 constexpr int ROWS_PER_PASS = 16; // so that PASSES * ROWS_PER_PASS rows make a block
-constexpr int HEADS_MAX = 24;  // of a thread block (12 frames of 3555 tokens: 157 us, with 8 heads 162)
-constexpr int SLOTS = 148 * 3;
-constexpr double START = 1.5;
+// Heads of a thread block, at most (12 frames of 3555 tokens, 24 heads: 157 us, with 8 heads
+// 162; more than 24 not measured).
+constexpr int HEADS_MAX = 24;
+constexpr int SLOTS = 148 * 3;  // blocks of 128 channels that run at once (of 64: twice as many, not counted)
+constexpr double START = 1.5;   // of a block, in heads
 static_assert(PASSES * ROWS_PER_PASS == CACHE8_BLOCK, "a block of tokens is held whole");
 
 struct AppendParams {
@@ -232,8 +235,9 @@ __global__ void __launch_bounds__(ROWS_PER_PASS * D / 8, 3 * 128 / D) cache8_app
 
 namespace {
 
-// Heads of a thread block: least rounds of the SLOTS blocks that run at once times
-// the heads of one and START more for its start; at most HEADS_MAX.
+// Heads of a thread block: least rounds of the SLOTS blocks (fractions counted, so that
+// 500 blocks are 1.13 rounds) times the heads of one and START more for its start; at
+// most HEADS_MAX.
 int heads_per_block(long long units, int H)
 {
     int best = 1;

@@ -15,13 +15,15 @@
 //   P V: the values go to bf16 code * scale (ra_cache8.cuh) and P to bf16, whose
 //        range no mixture of scales leaves, with or without what the rounding leaves
 //        (PForm).  For up to four queries the rests ride in the product's free
-//        columns: one query on 8 x 32768 keys 182 us, without them 179; a second
-//        product 197.  For eight it is a second product, asked for below 4096 keys.
+//        columns: the eight caches 182 us, without them 179; a second product 197.
+//        For more it is a second product, asked for below 4096 keys.
 // Ranges of keys leave partial (maximum, sum, O) to a second kernel that joins them.
-// Bound by memory for few queries (one byte a value of K and V): one query on each of
-// eight caches of 4096 to 32768 keys, 24 heads of 128, 179 us = 5.2 TB/s, 80 % of the
-// measured copy rate (DRAM traffic 0.938 GB of 0.934); the integer pipe, which turns
-// the codes of V to bf16, is 57 % busy.  One launch of a few hundred keys: 7 us.
+// Few queries read one byte a value of K and V: one query on each of eight caches of
+// 4096 to 32768 keys, 24 heads of 128, takes 182 us in a run of 30 calls = 5.1 TB/s, 78 %
+// of the measured copy rate, and 194 with caches that change from call to call (DRAM
+// traffic 0.939 GB of 0.934).  Nothing is at its limit: DRAM 65 % busy, the integer pipe,
+// which turns the codes of V to bf16, 60 %, issue slots 54 %, with 14 warps an SM.  One
+// launch of a few hundred keys: 7 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -527,9 +529,12 @@ __global__ void __launch_bounds__(128) cache8_join_kernel(const AttnParams p, lo
 }
 
 // How the work is cut.  Few queries: ranges of at least MIN_CHUNK keys, as many as
-// fill the SMs once, or several times where the ranges stay above LONG_CHUNK (batches
-// of unequal lengths balance better).  Many: the tiles a block (two, or one) and the
-// number of ranges with the least estimated time, one block an SM.
+// fill the SMs once (counted at the three blocks an SM of up to 8 queries; 9 to 16 have
+// two), or several times where the ranges stay above LONG_CHUNK (batches of unequal
+// lengths balance better).  Many: the tiles a block (two, or one) and the number of
+// ranges, up to 32, with the least estimated time, one block an SM.  (With one or two
+// heads more ranges would fill more SMs: 17 queries over 200000 keys of one head are an
+// estimated 92 us with 32 and 28 with 143.)
 constexpr int MIN_CHUNK = 256, LONG_CHUNK = 1024;
 constexpr int WHOLE = 512;  // as many keys as one block takes in less time than the join's launch
 constexpr int SMS = 148;
@@ -542,7 +547,7 @@ constexpr int WANT_BLOCKS = SMS * 16;
 constexpr int FEW_BLOCKS = 192;
 // A step of 64 keys, and a block's start and epilogue, as measured with a block on
 // each SM (12480 keys: two tiles 197 us with 64 channels and 231 with 128, one 113 and
-// 171); the join.  One tile a block wins where blocks are scarce or the last tile is
+// 171; P as one number); the join.  One tile a block wins where blocks are scarce or the last tile is
 // alone: 300 queries, 80 heads of 64, 12480 keys 253 -> 214 us; 256 queries, 24 heads
 // of 128, 512 keys 18.7 -> 14.6, but 12480 keys 62 -> 73.
 struct TileCost {
@@ -607,8 +612,8 @@ Plan plan_of(int B, int H, int d, int nq, int nk)
     pl.splits = pl.splits < 1 ? 1 : pl.splits;
     // One wave of blocks waits for its loads: the second group hides them (12480 keys, 24
     // heads of 128: 25 us, without it 27-29).  Several waves want more warps (eight caches
-    // of up to 32768 keys: 179 us, with it 189).  Sixteen queries need the registers for
-    // two groups either way (250 us; one group and 12 warps 273).
+    // of up to 32768 keys, P as one number: 179 us, with it 189).  Sixteen queries need the
+    // registers for two groups either way (250 us; one group and 12 warps 273).
     pl.ahead = nq > COLS || static_cast<long long>(pl.q_tiles) * pl.splits * H * B <= 2 * ONE_WAVE;
     pl.bytes = pl.splits == 1 ? 0 : static_cast<size_t>(B) * H * nq * pl.splits * (d + 2) * sizeof(float);
     return pl;

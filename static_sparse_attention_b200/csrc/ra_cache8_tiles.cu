@@ -22,7 +22,8 @@
 // the softmax of 2 x 128 x 64 scores and 1280 clocks of the tensor pipe.
 //
 // Measured: 1560 queries, 24960 keys, 40 heads of 128 (280 CTAs, two rounds of SMs)
-// 827 us = 964 TFLOP/s, 59 % of the measured bf16 burst; 2000 clocks a step, issue
+// 895 us in a run of 30 calls = 891 TFLOP/s, 55 % of the measured bf16 burst (921 with
+// rings that change from call to call; 827 on another GPU); 2000 clocks a step, issue
 // slots 67 %, exp2 and tensor pipes half busy each.  What a step waits for is the
 // softmax warps' own chain (1500 clocks of exponentials with the convert warps beside
 // them, 400 of barriers and TMEM).  On the way: one MMA warp for both tiles 1134 us (its
@@ -36,7 +37,8 @@
 // 1700 clocks; turns alone changed nothing, a fetch warp's own chain (waits, indexes,
 // factors) being as long.  With both, a step is 1000 clocks at 64 channels (issue
 // slots 67 %) and 1500 at 128, where the conversion is the longest (without it 1150).
-// 32 queries, 12480 keys: 80 heads of 64 113 -> 86 us, 192 heads of 128 269 -> 244.
+// 32 queries, 12480 keys: 80 heads of 64 113 -> 88 us, 192 heads of 128 269 -> 247.
+// All 128 rows of the tile are computed, however few of them are queries.
 //
 // A word of four codes is turned into two pairs, channels (0, 2) and (1, 3), which
 // saves the byte permutes.  So channels lie in the order 0, 2, 1, 3 within every

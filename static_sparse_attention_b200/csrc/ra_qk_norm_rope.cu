@@ -15,9 +15,9 @@
 // with its token and walks heads, so the cosines and sines of a token are
 // loaded once for many rows, which are fetched HEADS_IN_FLIGHT at a time.
 //
-// Measured: 108000 tokens, q and k of 24 heads of 128, 429 us = 6.2 TB/s, 94 % of the
+// Measured: 108000 tokens, q and k of 24 heads of 128, 428 us = 6.2 TB/s, 95 % of the
 // measured copy rate (DRAM traffic 2.60 GB of 2.65); backward of 63960 tokens, 40 heads
-// of 128, 709 us = 5.5 TB/s, 84 % (24 warps an SM; issue slots 68 % busy).
+// of 128, 702 us = 5.6 TB/s, 85 % (24 warps an SM; issue slots 68 % busy).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -413,7 +413,9 @@ ra_status check_sizes(int B, int n, int d, float eps)
 // 704 us against 758 with 8 heads at a time), else as many as cost least, in rounds
 // of the `slots` blocks that run at once (whole rounds where the blocks stay and take
 // several items each) times the batches of loads that a lane waits for, with a
-// quarter of one for the look-up of its angles.
+// quarter of one for the look-up of its angles.  (The backward plans each of its two
+// tensors as if it had all BWD_BLOCKS places, which the two share: one frame's rows, 792
+// blocks on 444 places, take 28.6 us of 14.8.)
 int heads_per_chunk(long long tiles, int B, int H, int slots, bool whole_rounds)
 {
     int best = H;
