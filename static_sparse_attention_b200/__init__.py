@@ -538,13 +538,19 @@ class SwcCache8:
         """One or more new frames (k, v: bf16 [B, frames * s, H, d]); of more than W
         the last W are kept."""
         _refuse_capture(stream)
+        self._used_on(stream)
+        self._append(k, v, k_weight, rope, eps, stream)
+
+    def _append(self, k, v, k_weight, rope, eps, stream) -> None:
         if k.dim() != 4 or v.shape != k.shape or k.shape[1] < self.s or k.shape[1] % self.s:
             raise ValueError(f"k and v must have shape [{self.B}, frames * {self.s}, {self.H}, {self.d}]")
         frames = k.shape[1] // self.s
-        skip = max(0, frames - self.W)
-        self._used_on(stream)
-        cache8_append(k[:, skip * self.s:], v[:, skip * self.s:], *self._ring, self.frames_seen + skip, k_weight, rope,
-                      eps, stream)
+        if frames > self.W:
+            skip = frames - self.W
+            k, v = k[:, skip * self.s:], v[:, skip * self.s:]
+        else:
+            skip = 0
+        cache8_append(k, v, *self._ring, self.frames_seen + skip, k_weight, rope, eps, stream)
         self.frames_seen += frames
 
     def attend(self, q, out=None, lse=None, scale: float | None = None, workspace=None, stream=None):
@@ -560,6 +566,7 @@ class SwcCache8:
         _refuse_capture(stream)
         if tuple(q.shape) != (self.B, self.s, self.H, self.d) or q.shape != k.shape:
             raise ValueError(f"q, k and v must have shape [{self.B}, {self.s}, {self.H}, {self.d}]")
+        self._used_on(stream)
         if q_weight is None and rope is None:
             with _allocating_on(stream, _stream_handle(stream)):
                 q = q.transpose(1, 2).contiguous()
@@ -571,9 +578,9 @@ class SwcCache8:
         if type(r) is int:
             check(r, "ra_cache8_attention")
         out, workspace = r
-        self.append(k, v, k_weight, rope, eps, stream)
+        self._append(k, v, k_weight, rope, eps, stream)
         try:
-            return self.attend(q, out, lse, scale, workspace, stream)
+            return cache8_attention(q, *self._ring, self.frames_held, None, scale, out, lse, workspace, stream)
         except Exception:
             self.frames_seen -= 1  # the launch failed: the next step takes the same slot
             raise
