@@ -275,9 +275,9 @@ __device__ __forceinline__ void group_step(State<D, NT>& st, const Group<D>& g, 
             if (P == P_PAIR) {
                 l0[t] = transpose8x8(y0);
                 l1[t] = transpose8x8(y1);
-            } else if (c >= 2) {  // queries 4-7 are queries 0-3 again
-                x0 = y0;
-                x1 = y1;
+            } else {  // queries 4-7, a lane's from c = 2 on, are queries 0-3 again
+                x0 = c < 2 ? x0 : y0;
+                x1 = c < 2 ? x1 : y1;
             }
         }
         b0[t] = transpose8x8(x0);
